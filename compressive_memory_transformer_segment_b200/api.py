@@ -10,6 +10,7 @@ Names follow the C ABI in include/infini_attn.h.
 
 import ctypes
 import os
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -87,6 +88,14 @@ _SIGNATURES = [
                                                _P, _P, _P, _P]),
     ("infini_attn_rope_tables", ctypes.c_int, [_P, _P, ctypes.c_int, ctypes.c_int, ctypes.c_double,
                                                _P]),
+    ("infini_attn_block_norm", ctypes.c_int, [_P, _P, _P, _P, _P, _P, ctypes.c_float,
+                                              ctypes.c_longlong, ctypes.c_int, ctypes.c_int,
+                                              _P, _P, _P, _P, _P]),
+    ("infini_attn_block_norm_backward_workspace_bytes", ctypes.c_size_t, [ctypes.c_longlong,
+                                                                           ctypes.c_int]),
+    ("infini_attn_block_norm_backward", ctypes.c_int, [_P] * 10 + [ctypes.c_longlong, ctypes.c_int,
+                                                                   ctypes.c_int] + [_P] * 7 +
+     [ctypes.c_size_t, _P]),
     ("infini_attn_backward", ctypes.c_int, [_P, _P, _P, _P, _P, _P, ctypes.c_int, ctypes.c_int,
                                             ctypes.POINTER(Dims), _P, _P, _P, _P, _P, _P, _P, _P,
                                             _P, _P, ctypes.c_size_t, _P]),
@@ -380,6 +389,131 @@ def qkv_project(x, w_qkv, bias, rope_cos, rope_sin, H_q, H_kv, d, q=None, k=None
     with _one_device(x, w_qkv, bias, rope_cos, rope_sin, q, k, v, stream=stream):
         _check(lib.infini_attn_qkv_project(*args, _stream_handle(stream)))
     return q, k, v
+
+
+# The entry points below are called once per token or per layer, where the
+# binding's own time counts: one check per tensor, plain integers as pointers,
+# and no device switch when the tensors' device is current already.
+
+
+def _arg(t, name, dtype, shape, dev):
+    """Address of a contiguous tensor of exactly this type, shape and device;
+    None for None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _cuda_device(t, name):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _empty(shape, dtype, dev, stream):
+    """New memory for an output that ``stream`` writes: of that stream's pool."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _call(fn, dev, stream, *args):
+    """fn(*args, stream handle) with the tensors' device current."""
+    if stream is None:
+        handle = torch.cuda.current_stream(dev).cuda_stream
+    elif stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+    else:
+        handle = stream.cuda_stream
+    if torch.cuda.current_device() == dev.index:
+        rc = fn(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, handle)
+    if rc != OK:
+        _check(rc)
+
+
+def block_norm(r, w_next, eps, o=None, gate=None, scale=None, w_post=None, r_out=None, h=None,
+               keep_rstd=True, stream=None):
+    """infini_attn_block_norm on CUDA tensors: r, o, gate [..., width] of one
+    dtype (bfloat16 or float32), scale, w_post, w_next float32 [width].
+    Returns (r_out, h, rstd_post, rstd_next): r_out is None without ``o``, h
+    without ``w_next``, and the reciprocal norms (float32 [...], for
+    block_norm_backward) without their weight or with ``keep_rstd=False``.
+    ``r_out`` may be ``r`` itself."""
+    dev, dt, shape = _cuda_device(r, "r"), r.dtype, r.shape
+    if dt not in DTYPES or r.dim() < 1:
+        raise ValueError("r must be [..., width], bfloat16 or float32")
+    width, f32 = shape[-1], torch.float32
+    vec, stat = (width,), shape[:-1]
+    if o is not None and r_out is None:
+        r_out = _empty(shape, dt, dev, stream)
+    if w_next is not None and h is None:
+        h = _empty(shape, dt, dev, stream)
+    rp = _empty(stat, f32, dev, stream) if keep_rstd and w_post is not None else None
+    rn = _empty(stat, f32, dev, stream) if keep_rstd and w_next is not None else None
+    _call(load_library().infini_attn_block_norm, dev, stream,
+          _arg(r, "r", dt, shape, dev), _arg(o, "o", dt, shape, dev), _arg(gate, "gate", dt, shape, dev),
+          _arg(scale, "scale", f32, vec, dev), _arg(w_post, "w_post", f32, vec, dev),
+          _arg(w_next, "w_next", f32, vec, dev), eps, r.numel() // max(width, 1), width, DTYPES[dt],
+          _arg(r_out, "r_out", dt, shape, dev), _arg(h, "h", dt, shape, dev),
+          rp.data_ptr() if rp is not None else None, rn.data_ptr() if rn is not None else None)
+    return r_out, h, rp, rn
+
+
+class BlockNormGrads(NamedTuple):
+    dr: Optional[torch.Tensor]
+    do: Optional[torch.Tensor]
+    dgate: Optional[torch.Tensor]
+    dscale: Optional[torch.Tensor]
+    dw_post: Optional[torch.Tensor]
+    dw_next: Optional[torch.Tensor]
+
+
+def block_norm_backward_workspace_bytes(rows, width):
+    return load_library().infini_attn_block_norm_backward_workspace_bytes(int(rows), int(width))
+
+
+def block_norm_backward(dr_out, dh, r_out, rstd_next, w_next, o=None, gate=None, scale=None,
+                        w_post=None, rstd_post=None, workspace=None, stream=None):
+    """infini_attn_block_norm_backward on CUDA tensors: the gradients of
+    block_norm's inputs from those of its outputs (``dr_out`` may be None for
+    zero; ``dh``, ``r_out`` and ``rstd_next`` are used with ``w_next`` only).
+    Returns BlockNormGrads; a gradient whose input was absent is None, and
+    without ``w_next`` dr is dr_out itself."""
+    lead = dr_out if dr_out is not None else dh
+    dev, dt, shape = _cuda_device(lead, "dr_out or dh"), lead.dtype, lead.shape
+    if dt not in DTYPES or lead.dim() < 1:
+        raise ValueError("gradients must be [..., width], bfloat16 or float32")
+    width, f32 = shape[-1], torch.float32
+    vec, stat = (width,), shape[:-1]
+    if w_next is None:
+        dh = r_out = rstd_next = None
+    if w_post is None:
+        rstd_post = None
+    dr = _empty(shape, dt, dev, stream) if w_next is not None else None
+    d_o = _empty(shape, dt, dev, stream) if o is not None else None
+    dgate = _empty(shape, dt, dev, stream) if gate is not None else None
+    dscale, dw_post, dw_next = (_empty(vec, f32, dev, stream) if w is not None else None
+                                for w in (scale, w_post, w_next))
+    ws, ws_n = None, 0
+    if workspace is not None:
+        ws, ws_n = _arg(workspace, "workspace", torch.uint8, (workspace.numel(),), dev), workspace.numel()
+    _call(load_library().infini_attn_block_norm_backward, dev, stream,
+          _arg(dr_out, "dr_out", dt, shape, dev), _arg(dh, "dh", dt, shape, dev),
+          _arg(r_out, "r_out", dt, shape, dev), _arg(o, "o", dt, shape, dev),
+          _arg(gate, "gate", dt, shape, dev), _arg(scale, "scale", f32, vec, dev),
+          _arg(w_post, "w_post", f32, vec, dev), _arg(w_next, "w_next", f32, vec, dev),
+          _arg(rstd_post, "rstd_post", f32, stat, dev), _arg(rstd_next, "rstd_next", f32, stat, dev),
+          lead.numel() // max(width, 1), width, DTYPES[dt],
+          *(t.data_ptr() if t is not None else None for t in (dr, d_o, dgate, dscale, dw_post, dw_next)),
+          ws, ws_n)
+    return BlockNormGrads(dr if dr is not None else dr_out, d_o, dgate, dscale, dw_post, dw_next)
 
 
 def decode_workspace_bytes(dims, seg_len, rule):

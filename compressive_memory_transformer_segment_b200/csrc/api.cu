@@ -779,6 +779,108 @@ int infini_attn_rope_tables(float* cos_out, float* sin_out, int n_pos, int d, do
              : INFINI_ERR_CUDA;
 }
 
+int infini_attn_block_norm(const void* r, const void* o, const void* gate, const float* scale,
+                           const float* w_post, const float* w_next, float eps, long long rows,
+                           int width, int dtype, void* r_out, void* h, float* rstd_post,
+                           float* rstd_next, void* stream) {
+  if (!r || rows < 1 || width < 1 || !(eps > 0.f) || eps > 3e38f) return INFINI_ERR_ARG;
+  if (dtype != INFINI_DTYPE_BF16 && dtype != INFINI_DTYPE_F32) return INFINI_ERR_ARG;
+  if (!o && (gate || scale || w_post)) return INFINI_ERR_ARG;
+  if ((o != nullptr) != (r_out != nullptr) || (w_next != nullptr) != (h != nullptr)) return INFINI_ERR_ARG;
+  if ((!o && !w_next) || (rstd_post && !w_post) || (rstd_next && !w_next)) return INFINI_ERR_ARG;
+  if (!block_norm_supported(width)) return INFINI_ERR_UNSUPPORTED;
+  const size_t elem = dtype == INFINI_DTYPE_BF16 ? 2 : 4;
+  if ((unsigned long long)rows > (1ull << 60) / ((size_t)width * elem)) return INFINI_ERR_ARG;
+  const size_t n = (size_t)rows * width * elem, nw = (size_t)width * 4, ns = (size_t)rows * 4;
+  const void* ptrs[] = {r, o, gate, scale, w_post, w_next, r_out, h, rstd_post, rstd_next};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return INFINI_ERR_ALIGN;
+  const Range ins[] = {rng(r, n), rng(o, o ? n : 0), rng(gate, gate ? n : 0), rng(scale, scale ? nw : 0),
+                       rng(w_post, w_post ? nw : 0), rng(w_next, w_next ? nw : 0)};
+  const Range outs[] = {rng(r_out, r_out ? n : 0), rng(h, h ? n : 0), rng(rstd_post, rstd_post ? ns : 0),
+                        rng(rstd_next, rstd_next ? ns : 0)};
+  for (int i = 0; i < 4; ++i) {
+    for (int j = 0; j < 6; ++j)
+      if (overlap(outs[i], ins[j]) && !(i == 0 && j == 0 && r_out == r)) return INFINI_ERR_ALIAS;
+    for (int j = i + 1; j < 4; ++j)
+      if (overlap(outs[i], outs[j])) return INFINI_ERR_ALIAS;
+  }
+  BlockNormProblem p = {};
+  p.r = r; p.o = o; p.gate = gate; p.scale = scale; p.w_post = w_post; p.w_next = w_next;
+  p.r_out = r_out; p.h = h; p.rstd_post = rstd_post; p.rstd_next = rstd_next;
+  p.rows = rows; p.width = width; p.eps = eps; p.bf16 = dtype == INFINI_DTYPE_BF16;
+  return launch_block_norm_forward(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? INFINI_OK
+                                                                                        : INFINI_ERR_CUDA;
+}
+
+size_t infini_attn_block_norm_backward_workspace_bytes(long long rows, int width) {
+  if (rows < 1 || width < 1 || !block_norm_supported(width)) return 0;
+  return align_up((size_t)block_norm_partials(rows, width) * 2 * width * 4);
+}
+
+int infini_attn_block_norm_backward(const void* dr_out, const void* dh, const void* r_out, const void* o,
+                                    const void* gate, const float* scale, const float* w_post,
+                                    const float* w_next, const float* rstd_post,
+                                    const float* rstd_next, long long rows, int width, int dtype,
+                                    void* dr, void* d_o, void* dgate, float* dscale, float* dw_post,
+                                    float* dw_next, void* workspace, size_t workspace_bytes,
+                                    void* stream) {
+  if (rows < 1 || width < 1) return INFINI_ERR_ARG;
+  if (dtype != INFINI_DTYPE_BF16 && dtype != INFINI_DTYPE_F32) return INFINI_ERR_ARG;
+  if ((!o && !w_next) || (!o && (gate || scale || w_post)) || (!dr_out && !w_next)) return INFINI_ERR_ARG;
+  const bool next = w_next != nullptr;
+  const void* with_next[] = {dh, r_out, rstd_next, dr, dw_next};
+  for (const void* p : with_next)
+    if ((p != nullptr) != next) return INFINI_ERR_ARG;
+  if ((d_o != nullptr) != (o != nullptr) || (dgate != nullptr) != (gate != nullptr) ||
+      (dscale != nullptr) != (scale != nullptr) || (dw_post != nullptr) != (w_post != nullptr) ||
+      (rstd_post != nullptr) != (w_post != nullptr))
+    return INFINI_ERR_ARG;
+  if (!block_norm_supported(width)) return INFINI_ERR_UNSUPPORTED;
+  const size_t elem = dtype == INFINI_DTYPE_BF16 ? 2 : 4;
+  if ((unsigned long long)rows > (1ull << 60) / ((size_t)width * elem)) return INFINI_ERR_ARG;
+  const void* ptrs[] = {dr_out, dh, r_out, o, gate, scale, w_post, w_next, rstd_post, rstd_next,
+                        dr, d_o, dgate, dscale, dw_post, dw_next};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return INFINI_ERR_ALIGN;
+  const size_t total = infini_attn_block_norm_backward_workspace_bytes(rows, width);
+  if (workspace == nullptr && workspace_bytes != 0) return INFINI_ERR_ARG;
+  if (workspace && (workspace_bytes < total || ((uintptr_t)workspace & (kAlign - 1)) != 0))
+    return INFINI_ERR_WORKSPACE;
+  const size_t n = (size_t)rows * width * elem, nw = (size_t)width * 4, ns = (size_t)rows * 4;
+  auto opt = [](const void* p, size_t bytes) { return rng(p, p ? bytes : 0); };
+  const Range ins[] = {opt(dr_out, n), opt(dh, n), opt(r_out, n), opt(o, n), opt(gate, n), opt(scale, nw),
+                       opt(w_post, nw), opt(w_next, nw), opt(rstd_post, ns), opt(rstd_next, ns)};
+  const Range outs[] = {opt(dr, n), opt(d_o, n), opt(dgate, n), opt(dscale, nw), opt(dw_post, nw),
+                        opt(dw_next, nw), opt(workspace, total)};
+  for (int i = 0; i < 7; ++i) {
+    for (int j = 0; j < 10; ++j)
+      if (overlap(outs[i], ins[j]) && !(i == 0 && j == 0 && dr == dr_out)) return INFINI_ERR_ALIAS;
+    for (int j = i + 1; j < 7; ++j)
+      if (overlap(outs[i], outs[j])) return INFINI_ERR_ALIAS;
+  }
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  char* ws = static_cast<char*>(workspace);
+  bool owned = false;
+  if (!ws) {
+    if (cudaMallocAsync(reinterpret_cast<void**>(&ws), total, st) != cudaSuccess) return INFINI_ERR_CUDA;
+    owned = true;
+  }
+  BlockNormProblem p = {};
+  p.r = r_out; p.o = o; p.gate = gate; p.scale = scale; p.w_post = w_post; p.w_next = w_next;
+  p.rstd_post = const_cast<float*>(rstd_post); p.rstd_next = const_cast<float*>(rstd_next);
+  p.dr_out = dr_out; p.dh = dh; p.dr = dr; p.d_o = d_o; p.dgate = dgate;
+  p.dscale = dscale; p.dw_post = dw_post; p.dw_next = dw_next;
+  p.part = reinterpret_cast<float*>(ws);
+  p.rows = rows; p.width = width; p.bf16 = dtype == INFINI_DTYPE_BF16;
+  cudaError_t e = launch_block_norm_backward(p, st);
+  if (owned) {
+    cudaError_t f = cudaFreeAsync(ws, st);
+    if (e == cudaSuccess) e = f;
+  }
+  return e == cudaSuccess ? INFINI_OK : INFINI_ERR_CUDA;
+}
+
 int infini_attn_sync_status(void* stream) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (cudaStreamSynchronize(st) != cudaSuccess) return INFINI_ERR_CUDA;

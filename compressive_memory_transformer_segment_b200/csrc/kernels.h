@@ -132,6 +132,39 @@ cudaError_t launch_qkv_projection(const ProjectionProblem& p, cudaStream_t strea
 cudaError_t launch_rope_tables(float* cos_out, float* sin_out, int n_pos, int d, double base,
                                cudaStream_t stream);
 
+// Norms around the layer with the block's gate, residual scale and residual
+// sum.  Pointers that a call does not use are null.
+constexpr int kBlockNormMaxWidth = 16384;
+struct BlockNormProblem {
+  const void* r;          // forward: [rows][width] stream; backward: r_out, read if w_next
+  const void* o;          // [rows][width] block output or null
+  const void* gate;       // [rows][width] gate logits or null
+  const float* scale;     // [width] or null (1)
+  const float* w_post;    // [width] or null (no norm of o)
+  const float* w_next;    // [width] or null (no next norm)
+  void* r_out;            // forward outputs
+  void* h;
+  float* rstd_post;       // [rows]; forward outputs (null: not kept), backward inputs
+  float* rstd_next;
+  const void* dr_out;     // backward inputs
+  const void* dh;
+  void* dr;               // backward outputs
+  void* d_o;
+  void* dgate;
+  float* dscale;          // [width]
+  float* dw_post;
+  float* dw_next;
+  float* part;            // workspace: [partials][2][width]
+  long long rows;
+  int width;
+  float eps;
+  bool bf16;
+};
+bool block_norm_supported(int width);
+int block_norm_partials(long long rows, int width);
+cudaError_t launch_block_norm_forward(const BlockNormProblem& p, cudaStream_t stream);
+cudaError_t launch_block_norm_backward(const BlockNormProblem& p, cudaStream_t stream);
+
 int decode_splits(int S);
 int decode_head_chunks(int g);
 cudaError_t launch_decode_step(const DecodeProblem& p, cudaStream_t stream);

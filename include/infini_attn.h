@@ -291,6 +291,83 @@ INFINI_API int infini_attn_qkv_project(const void* x, const void* w_qkv, const f
 INFINI_API int infini_attn_rope_tables(float* cos_out, float* sin_out, int n_pos, int d,
                                        double base, void* stream);
 
+/* Norms before and after the layer, fused with the block's gate, residual
+ * scale and residual sum.  The reproduction trains Llama models ("Hugging Face
+ * Infini-Attention 再現分析"), whose layers read a root-mean-square norm of the
+ * residual stream and add their projected output to it; the norm after the
+ * block, the gate and the scale are a reading (the pages define none).
+ * For each of `rows` tokens of `width` channels (mean over the channels):
+ *   n     = w_post ? o / sqrt(mean(o^2) + eps) * w_post : o
+ *   r_out = r + scale * sg(gate) * n      (scale = 1, sg(gate) = 1 if NULL)
+ *   h     = r_out / sqrt(mean(r_out^2) + eps) * w_next
+ * with o == NULL: h is the norm of r alone; with w_next == NULL: r_out alone.
+ * h is computed from the sum before its rounding to dtype.
+ *   r            device [rows, width], the residual stream, element type dtype
+ *   o            device [rows, width], the block's output, or NULL
+ *   gate         device [rows, width], gate logits, or NULL
+ *   scale        device float32 [width], residual scale, or NULL
+ *   w_post       device float32 [width], weight of the norm of o, or NULL
+ *   w_next       device float32 [width], weight of the next norm, or NULL
+ *   eps          > 0, finite
+ *   r_out        device [rows, width] if o is given, else NULL; may equal r
+ *                (the stream updated in place)
+ *   h            device [rows, width] if w_next is given, else NULL
+ *   rstd_post    device float32 [rows], 1 / sqrt(mean(o^2) + eps), for the
+ *                backward; NULL: not kept.  Only with w_post.
+ *   rstd_next    likewise for the next norm.  Only with w_next.
+ *   stream       cudaStream_t; asynchronous, no workspace.
+ * Rows do not affect one another.  Squares are summed in fp32: |values|
+ * beyond 1e18 overflow the mean.  Supported: width <= 16384
+ * (INFINI_ERR_UNSUPPORTED beyond); rows whose byte size is a multiple of 16
+ * are read in 16-byte pieces, others element by element.  Errors:
+ * INFINI_ERR_ARG (NULL r, a size < 1, eps, gate / scale / w_post / rstd
+ * without what they belong to, a missing or extra output),
+ * INFINI_ERR_ALIGN, INFINI_ERR_ALIAS (any overlap of an output but r_out ==
+ * r), INFINI_ERR_CUDA. */
+INFINI_API int infini_attn_block_norm(const void* r, const void* o, const void* gate,
+                                      const float* scale, const float* w_post, const float* w_next,
+                                      float eps, long long rows, int width, int dtype, void* r_out,
+                                      void* h, float* rstd_post, float* rstd_next, void* stream);
+
+/* Bytes of device workspace infini_attn_block_norm_backward needs (0 if the
+ * sizes are invalid). */
+INFINI_API size_t infini_attn_block_norm_backward_workspace_bytes(long long rows, int width);
+
+/* Backward of infini_attn_block_norm: given the gradients of a scalar loss
+ * with respect to r_out and h, writes its gradients with respect to r, o,
+ * gate, scale, w_post and w_next.
+ *   dr_out       device [rows, width], element type dtype, or NULL for zero
+ *                (not NULL if w_next is NULL)
+ *   dh           device [rows, width]; with w_next only
+ *   r_out        the forward's r_out (r itself if o was NULL); with w_next only
+ *   o, gate, scale, w_post, w_next
+ *                the forward's arguments
+ *   rstd_post, rstd_next
+ *                what the forward kept
+ *   dr           device [rows, width]; with w_next only (without it, dr is
+ *                dr_out); may equal dr_out
+ *   d_o, dgate   device [rows, width]; with o, with gate
+ *   dscale, dw_post, dw_next
+ *                device float32 [width], summed over the rows; each with its
+ *                vector
+ *   workspace    device scratch of
+ *                infini_attn_block_norm_backward_workspace_bytes bytes,
+ *                256-byte aligned (its previous contents do not matter), or
+ *                NULL with workspace_bytes == 0 (taken on `stream`)
+ *   stream       cudaStream_t; asynchronous.
+ * A pointer that the call does not use must be NULL.  Sums run in fp32 in a
+ * fixed order: repeated calls give bitwise identical gradients.  Errors:
+ * those of infini_attn_block_norm and INFINI_ERR_WORKSPACE; of the overlaps
+ * only dr == dr_out is allowed. */
+INFINI_API int infini_attn_block_norm_backward(const void* dr_out, const void* dh, const void* r_out,
+                                               const void* o, const void* gate, const float* scale,
+                                               const float* w_post, const float* w_next,
+                                               const float* rstd_post, const float* rstd_next,
+                                               long long rows, int width, int dtype, void* dr,
+                                               void* d_o, void* dgate, float* dscale,
+                                               float* dw_post, float* dw_next, void* workspace,
+                                               size_t workspace_bytes, void* stream);
+
 /* Streaming decode: the layer forward one token at a time.  The current
  * segment's keys and values so far are kept by the caller in a rolling
  * buffer of seg_len rows per KV head; (M, z) hold the memory of the segments

@@ -22,6 +22,9 @@ The prologue (``infini_projection``: rope_angles, rope_tables, apply_rope,
 qkv_projection, qkv_project_rope) is pinned in
 ``tests/test_oracle_projection.py`` against brute-force loops, the complex
 form of the rotation and its invariants.
+The norms around the layer (``infini_block_norm``: block_norm,
+block_norm_vjp) are pinned in ``tests/test_oracle_block_norm.py`` against loops
+over single elements and central finite differences.
 No function here is "parity unpinned".
 """
 
@@ -50,4 +53,8 @@ from .infini_projection import (  # noqa: F401
     apply_rope,
     qkv_projection,
     qkv_project_rope,
+)
+from .infini_block_norm import (  # noqa: F401
+    block_norm,
+    block_norm_vjp,
 )

@@ -247,6 +247,63 @@ def test_qkv_project_and_rope_tables_check_arguments_on_the_host(lib):
     assert lib.infini_attn_rope_tables(P(MB), P(MB + 256), 16, 64, 1e4, P(0)) == api.ERR_ALIAS
 
 
+def test_block_norm_checks_arguments_on_the_host(lib):
+    """Argument checks of the norms around the layer return before any CUDA
+    call (addresses are never dereferenced)."""
+    MB = 1 << 20
+    good = dict(r=1 * MB, o=2 * MB, gate=3 * MB, scale=4 * MB, w_post=5 * MB, w_next=6 * MB, eps=1e-6,
+                rows=64, width=256, dtype=0, r_out=7 * MB, h=8 * MB, rp=9 * MB, rn=10 * MB)
+
+    def call(**over):
+        return lib.infini_attn_block_norm(*dict(good, **over).values(), None)
+
+    assert call(r=None) == api.ERR_ARG
+    assert call(rows=0) == api.ERR_ARG
+    assert call(width=0) == api.ERR_ARG
+    for eps in (0.0, -1.0, float("nan"), float("inf")):
+        assert call(eps=eps) == api.ERR_ARG
+    assert call(dtype=2) == api.ERR_ARG
+    assert call(o=None) == api.ERR_ARG                       # gate, scale, w_post belong to o
+    assert call(r_out=None) == api.ERR_ARG
+    assert call(w_next=None) == api.ERR_ARG                  # h without its weight
+    assert call(w_next=None, h=None) == api.ERR_ARG          # rstd_next without its weight
+    assert call(w_post=None) == api.ERR_ARG                  # rstd_post without its weight
+    assert call(o=None, gate=None, scale=None, w_post=None, r_out=None, rp=None, w_next=None, h=None,
+                rn=None) == api.ERR_ARG                      # nothing to do
+    assert call(width=16385) == api.ERR_UNSUPPORTED
+    assert call(rows=1 << 59) == api.ERR_ARG
+    assert call(h=8 * MB + 8) == api.ERR_ALIGN
+    assert call(h=good["o"] + 1024) == api.ERR_ALIAS
+    assert call(r_out=good["r"] + 512) == api.ERR_ALIAS      # in place means the same pointer
+    assert call(rn=good["rp"] + 16) == api.ERR_ALIAS
+
+    assert lib.infini_attn_block_norm_backward_workspace_bytes(0, 256) == 0
+    assert lib.infini_attn_block_norm_backward_workspace_bytes(64, 16385) == 0
+    n = lib.infini_attn_block_norm_backward_workspace_bytes(64, 256)
+    assert n >= 64 * 2 * 256 * 4
+    # never more than the resident blocks' shares
+    assert lib.infini_attn_block_norm_backward_workspace_bytes(1 << 30, 4096) <= 1 << 28
+    bwd = dict(dr_out=1 * MB, dh=2 * MB, r_out=3 * MB, o=4 * MB, gate=5 * MB, scale=6 * MB, w_post=7 * MB,
+               w_next=8 * MB, rp=9 * MB, rn=10 * MB, rows=64, width=256, dtype=0, dr=11 * MB, d_o=12 * MB,
+               dgate=13 * MB, dscale=14 * MB, dw_post=15 * MB, dw_next=16 * MB, ws=32 * MB, ws_n=n)
+
+    def back(**over):
+        return lib.infini_attn_block_norm_backward(*dict(bwd, **over).values(), None)
+
+    for name in ("dh", "r_out", "rn", "dr", "dw_next", "rp", "d_o", "dgate", "dscale", "dw_post"):
+        assert back(**{name: None}) == api.ERR_ARG, name
+    assert back(o=None) == api.ERR_ARG
+    assert back(dr_out=None, w_next=None, dh=None, r_out=None, rn=None, dr=None, dw_next=None) == api.ERR_ARG
+    assert back(width=16385) == api.ERR_UNSUPPORTED
+    assert back(dgate=13 * MB + 4) == api.ERR_ALIGN
+    assert back(ws_n=n - 1) == api.ERR_WORKSPACE
+    assert back(ws=32 * MB + 16) == api.ERR_WORKSPACE
+    assert back(ws=None) == api.ERR_ARG
+    assert back(d_o=bwd["dgate"] + 64) == api.ERR_ALIAS
+    assert back(dr=bwd["dr_out"] + 64) == api.ERR_ALIAS
+    assert back(ws=bwd["dr"]) == api.ERR_ALIAS
+
+
 def test_plain_c_program_uses_the_boundary(tmp_path):
     """The header compiles as C99 and a C program linked against the library
     gets the documented answers from the host-side calls (no GPU needed)."""
