@@ -25,6 +25,7 @@ OK = 0
 ERR_ARG, ERR_UNSUPPORTED, ERR_ALIAS, ERR_CUDA, ERR_TIMEOUT, ERR_WORKSPACE, ERR_ALIGN = (
     -1, -2, -3, -4, -5, -6, -7)
 ERR_SCRATCH_LIMIT = -8
+ERR_RANGE = -9
 
 
 class Dims(ctypes.Structure):
@@ -96,6 +97,12 @@ _SIGNATURES = [
     ("infini_attn_block_norm_backward", ctypes.c_int, [_P] * 10 + [ctypes.c_longlong, ctypes.c_int,
                                                                    ctypes.c_int] + [_P] * 7 +
      [ctypes.c_size_t, _P]),
+    ("infini_attn_w4_quantize", ctypes.c_int, [_P] + [ctypes.c_int] * 4 + [_P] * 4),
+    ("infini_attn_w4_pack", ctypes.c_int, [_P, ctypes.c_int, ctypes.c_int, _P, _P]),
+    ("infini_attn_w4_dequantize", ctypes.c_int, [_P] * 3 + [ctypes.c_int] * 4 + [_P] * 2),
+    ("infini_attn_linear_w4", ctypes.c_int, [_P] * 5 + [ctypes.c_int] * 5 + [_P] * 2),
+    ("infini_attn_qkv_project_w4", ctypes.c_int, [_P] * 7 + [ctypes.c_int, _P, ctypes.POINTER(Dims),
+                                                             ctypes.c_int, ctypes.c_int] + [_P] * 4),
     ("infini_attn_backward", ctypes.c_int, [_P, _P, _P, _P, _P, _P, ctypes.c_int, ctypes.c_int,
                                             ctypes.POINTER(Dims), _P, _P, _P, _P, _P, _P, _P, _P,
                                             _P, _P, ctypes.c_size_t, _P]),
@@ -514,6 +521,115 @@ def block_norm_backward(dr_out, dh, r_out, rstd_next, w_next, o=None, gate=None,
           *(t.data_ptr() if t is not None else None for t in (dr, d_o, dgate, dscale, dw_post, dw_next)),
           ws, ws_n)
     return BlockNormGrads(dr if dr is not None else dr_out, d_o, dgate, dscale, dw_post, dw_next)
+
+
+def _w4_shapes(N, K, group):
+    blocks = -(-K // 128)
+    return (N, blocks * 64), (N, blocks * 128 // group)
+
+
+def w4_quantize(w, group=128, zeros=True, stream=None):
+    """infini_attn_w4_quantize: w [N, K] (bfloat16 or float32 CUDA) to
+    (packed uint8 [N, 64 ceil(K / 128)], scales bfloat16 and zeros uint8
+    [N, ceil(K / 128) 128 / group]); zeros is None with ``zeros=False``."""
+    dev = _cuda_device(w, "w")
+    if w.dim() != 2 or w.dtype not in DTYPES or group not in (32, 64, 128):
+        raise ValueError("w must be [N, K], bfloat16 or float32, and group 32, 64 or 128")
+    N, K = w.shape
+    ps, gs = _w4_shapes(N, K, group)
+    packed = _empty(ps, torch.uint8, dev, stream)
+    scales = _empty(gs, torch.bfloat16, dev, stream)
+    z = _empty(gs, torch.uint8, dev, stream) if zeros else None
+    _call(load_library().infini_attn_w4_quantize, dev, stream, _arg(w, "w", w.dtype, (N, K), dev), N, K,
+          group, DTYPES[w.dtype], packed.data_ptr(), scales.data_ptr(), z.data_ptr() if zeros else None)
+    return packed, scales, z
+
+
+def w4_pack(codes, stream=None):
+    """infini_attn_w4_pack: codes uint8 [N, K] (0..15) to packed uint8
+    [N, 64 ceil(K / 128)]."""
+    dev = _cuda_device(codes, "codes")
+    if codes.dim() != 2:
+        raise ValueError("codes must be [N, K]")
+    N, K = codes.shape
+    packed = _empty(_w4_shapes(N, K, 128)[0], torch.uint8, dev, stream)
+    _call(load_library().infini_attn_w4_pack, dev, stream, _arg(codes, "codes", torch.uint8, (N, K), dev),
+          N, K, packed.data_ptr())
+    return packed
+
+
+class LinearW4:
+    """A linear layer with 4-bit weights (infini_attn_linear_w4 and
+    infini_attn_qkv_project_w4): ``packed``, ``scales`` and ``zeros`` (or None)
+    in the library's layout for K input channels, ``bias`` float32 [N] or None.
+    The tensors are checked once, here; the object keeps them."""
+
+    def __init__(self, packed, scales, zeros, K, bias=None):
+        dev = self.device = _cuda_device(packed, "packed")
+        if packed.dim() != 2 or scales.dim() != 2 or int(K) < 1:
+            raise ValueError("packed must be [N, 64 ceil(K / 128)] and scales [N, groups]")
+        self.N, self.K = packed.shape[0], int(K)
+        padded = -(-self.K // 128) * 128
+        groups = scales.shape[1]
+        self.group = padded // groups if groups and padded % groups == 0 else 0
+        if self.group not in (32, 64, 128):
+            raise ValueError("scales must have ceil(K / 128) * 128 / group columns, group 32, 64 or 128")
+        ps, gs = _w4_shapes(self.N, self.K, self.group)
+        self.packed, self.scales, self.zeros, self.bias = packed, scales, zeros, bias
+        self._weights = (_arg(packed, "packed", torch.uint8, ps, dev),
+                         _arg(scales, "scales", torch.bfloat16, gs, dev),
+                         _arg(zeros, "zeros", torch.uint8, gs, dev),
+                         _arg(bias, "bias", torch.float32, (self.N,), dev))
+        self._lib = load_library()
+
+    @classmethod
+    def from_weight(cls, w, group=128, zeros=True, bias=None, stream=None):
+        """Quantise w [N, K]."""
+        return cls(*w4_quantize(w, group, zeros, stream=stream), w.shape[1], bias=bias)
+
+    def dequantize(self, dtype=torch.float32, stream=None):
+        """The weights [N, K] as the layer uses them."""
+        w = _empty((self.N, self.K), dtype, self.device, stream)
+        _call(self._lib.infini_attn_w4_dequantize, self.device, stream, *self._weights[:3], self.N, self.K,
+              self.group, DTYPES[dtype], w.data_ptr())
+        return w
+
+    def __call__(self, x, out=None, stream=None):
+        """x [..., K], bfloat16 or float32, to [..., N] of the same type."""
+        dt, shape = x.dtype, x.shape
+        if dt not in DTYPES or not shape or shape[-1] != self.K:
+            raise ValueError(f"x must be [..., {self.K}], bfloat16 or float32")
+        ys = (*shape[:-1], self.N)
+        y = _empty(ys, dt, self.device, stream) if out is None else out
+        _call(self._lib.infini_attn_linear_w4, self.device, stream, _arg(x, "x", dt, shape, self.device),
+              *self._weights, x.numel() // self.K, self.N, self.K, self.group, DTYPES[dt],
+              y.data_ptr() if out is None else _arg(out, "out", dt, ys, self.device))
+        return y
+
+    def qkv(self, x, H_q, H_kv, d, rope_cos=None, rope_sin=None, positions=None, q=None, k=None, v=None,
+            stream=None):
+        """x [B, L, K] to the heads q [B, H_q, L, d], k, v [B, H_kv, L, d],
+        queries and keys rotated by rows ``positions`` (int32 [B, L]; None:
+        0 .. L - 1) of the float32 tables [n_pos, d / 2]."""
+        dev, dt = self.device, x.dtype
+        if dt not in DTYPES or x.dim() != 3 or x.shape[2] != self.K or (H_q + 2 * H_kv) * d != self.N:
+            raise ValueError(f"x must be [B, L, {self.K}], bfloat16 or float32, and (H_q + 2 H_kv) d = {self.N}")
+        if (rope_cos is None) != (rope_sin is None):
+            raise ValueError("give both rotary tables or neither")
+        B, L, _ = x.shape
+        qs, ks = (B, H_q, L, d), (B, H_kv, L, d)
+        q = _empty(qs, dt, dev, stream) if q is None else q
+        k = _empty(ks, dt, dev, stream) if k is None else k
+        v = _empty(ks, dt, dev, stream) if v is None else v
+        n_pos = rope_cos.shape[0] if rope_cos is not None else 0
+        rot = (n_pos, d // 2)
+        dims = Dims(B, H_q, H_kv, L, d, d, DTYPES[dt])
+        _call(self._lib.infini_attn_qkv_project_w4, dev, stream, _arg(x, "x", dt, x.shape, dev),
+              *self._weights, _arg(rope_cos, "rope_cos", torch.float32, rot, dev),
+              _arg(rope_sin, "rope_sin", torch.float32, rot, dev), n_pos,
+              _arg(positions, "positions", torch.int32, (B, L), dev), ctypes.byref(dims), self.K, self.group,
+              _arg(q, "q", dt, qs, dev), _arg(k, "k", dt, ks, dev), _arg(v, "v", dt, ks, dev))
+        return q, k, v
 
 
 def decode_workspace_bytes(dims, seg_len, rule):

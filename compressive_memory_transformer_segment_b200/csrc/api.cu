@@ -222,6 +222,8 @@ const char* infini_attn_status_string(int status) {
     case INFINI_ERR_SCRATCH_LIMIT:
       return "problem needs more scratch than the no-allocation entry point's static array "
              "holds; use infini_attn_forward with a workspace";
+    case INFINI_ERR_RANGE:
+      return "a position read from device memory was outside its range (device status word set)";
     default: return "unknown status";
   }
 }
@@ -881,6 +883,149 @@ int infini_attn_block_norm_backward(const void* dr_out, const void* dh, const vo
   return e == cudaSuccess ? INFINI_OK : INFINI_ERR_CUDA;
 }
 
+namespace {
+
+constexpr int kW4Block = 128;  // channels of a packed block
+
+// Sizes of a 4-bit weight matrix; INFINI_OK or the error for them.
+struct W4Shape {
+  size_t packed, scales, zeros;  // bytes
+};
+
+int w4_shape(long long N, int K, int group, W4Shape* s) {
+  if (N < 1 || K < 1 || group < 1) return INFINI_ERR_ARG;
+  if (K % 8 != 0 || (group != 32 && group != 64 && group != 128) || N > 0x7fffffffLL - 64 ||
+      K > 0x7fffffff - kW4Block)
+    return INFINI_ERR_UNSUPPORTED;
+  const size_t blocks = ((size_t)K + kW4Block - 1) / kW4Block;
+  s->packed = (size_t)N * blocks * (kW4Block / 2);
+  s->zeros = (size_t)N * blocks * (kW4Block / group);
+  s->scales = s->zeros * 2;
+  return INFINI_OK;
+}
+
+int w4_run(const W4Problem& p, cudaStream_t st) {
+  return launch_w4(p, st) == cudaSuccess ? INFINI_OK : INFINI_ERR_CUDA;
+}
+
+int w4_layout(const void* w, size_t w_bytes, bool w_written, void* packed, void* scales, void* zeros,
+              int N, int K, int group, int dtype, W4Layout what, void* stream) {
+  W4Shape s;
+  if (dtype != INFINI_DTYPE_BF16 && dtype != INFINI_DTYPE_F32) return INFINI_ERR_ARG;
+  const void* ptrs[] = {w, packed, scales, zeros};
+  int rc = w4_shape(N, K, group, &s);
+  if (rc != INFINI_OK) return rc;
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return INFINI_ERR_ALIGN;
+  const Range r[] = {rng(w, w_bytes), rng(packed, s.packed), rng(scales, scales ? s.scales : 0),
+                     rng(zeros, zeros ? s.zeros : 0)};
+  for (int i = 0; i < 4; ++i)
+    for (int j = i + 1; j < 4; ++j)
+      if ((i == 0 || !w_written) && overlap(r[i], r[j])) return INFINI_ERR_ALIAS;
+  W4PackProblem p;
+  p.w = w; p.packed = static_cast<uint8_t*>(packed); p.scales = static_cast<__nv_bfloat16*>(scales);
+  p.zeros = static_cast<uint8_t*>(zeros); p.N = N; p.K = K; p.group = group;
+  p.bf16 = dtype == INFINI_DTYPE_BF16;
+  return launch_w4_layout(p, what, static_cast<cudaStream_t>(stream)) == cudaSuccess ? INFINI_OK
+                                                                                     : INFINI_ERR_CUDA;
+}
+
+}  // namespace
+
+int infini_attn_w4_quantize(const void* w, int N, int K, int group, int dtype, void* packed, void* scales,
+                            void* zeros, void* stream) {
+  if (!w || !packed || !scales) return INFINI_ERR_ARG;
+  const size_t elem = dtype == INFINI_DTYPE_BF16 ? 2 : 4;
+  return w4_layout(w, N > 0 && K > 0 ? (size_t)N * K * elem : 0, false, packed, scales, zeros, N, K, group,
+                   dtype, W4Layout::kQuantize, stream);
+}
+
+int infini_attn_w4_pack(const void* codes, int N, int K, void* packed, void* stream) {
+  if (!codes || !packed) return INFINI_ERR_ARG;
+  return w4_layout(codes, N > 0 && K > 0 ? (size_t)N * K : 0, false, packed, nullptr, nullptr, N, K, 128,
+                   INFINI_DTYPE_BF16, W4Layout::kPack, stream);
+}
+
+int infini_attn_w4_dequantize(const void* packed, const void* scales, const void* zeros, int N, int K,
+                              int group, int dtype, void* w, void* stream) {
+  if (!w || !packed || !scales) return INFINI_ERR_ARG;
+  const size_t elem = dtype == INFINI_DTYPE_BF16 ? 2 : 4;
+  return w4_layout(w, N > 0 && K > 0 ? (size_t)N * K * elem : 0, true, const_cast<void*>(packed),
+                   const_cast<void*>(scales), const_cast<void*>(zeros), N, K, group, dtype,
+                   W4Layout::kDequantize, stream);
+}
+
+int infini_attn_linear_w4(const void* x, const void* packed, const void* scales, const void* zeros,
+                          const float* bias, int M, int N, int K, int group, int dtype, void* y,
+                          void* stream) {
+  if (!x || !packed || !scales || !y || M < 1) return INFINI_ERR_ARG;
+  if (dtype != INFINI_DTYPE_BF16 && dtype != INFINI_DTYPE_F32) return INFINI_ERR_ARG;
+  W4Shape s;
+  int rc = w4_shape(N, K, group, &s);
+  if (rc != INFINI_OK) return rc;
+  if (M > 65535 * 64) return INFINI_ERR_UNSUPPORTED;
+  const size_t elem = dtype == INFINI_DTYPE_BF16 ? 2 : 4;
+  const void* ptrs[] = {x, packed, scales, zeros, bias, y};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return INFINI_ERR_ALIGN;
+  const Range ins[] = {rng(x, (size_t)M * K * elem), rng(packed, s.packed), rng(scales, s.scales),
+                       rng(zeros, zeros ? s.zeros : 0), rng(bias, bias ? (size_t)N * 4 : 0)};
+  for (const Range& r : ins)
+    if (overlap(rng(y, (size_t)M * N * elem), r)) return INFINI_ERR_ALIAS;
+  W4Problem p = {};
+  p.x = x; p.packed = static_cast<const uint8_t*>(packed);
+  p.scales = static_cast<const __nv_bfloat16*>(scales); p.zeros = static_cast<const uint8_t*>(zeros);
+  p.bias = bias; p.y = y; p.M = M; p.N = N; p.K = K; p.group = group; p.L = 1;
+  p.bf16 = dtype == INFINI_DTYPE_BF16;
+  return w4_run(p, static_cast<cudaStream_t>(stream));
+}
+
+int infini_attn_qkv_project_w4(const void* x, const void* packed, const void* scales, const void* zeros,
+                               const float* bias, const float* rope_cos, const float* rope_sin, int n_pos,
+                               const int* positions, const infini_dims_t* dims, int d_model, int group,
+                               void* q, void* k, void* v, void* stream) {
+  if (!dims || !x || !packed || !scales || !q || !k || !v) return INFINI_ERR_ARG;
+  if ((rope_cos == nullptr) != (rope_sin == nullptr)) return INFINI_ERR_ARG;
+  if (dims->B < 1 || dims->H_q < 1 || dims->H_kv < 1 || dims->L < 1 || d_model < 1) return INFINI_ERR_ARG;
+  if (rope_cos && (n_pos < 1 || (!positions && n_pos < dims->L))) return INFINI_ERR_ARG;
+  if (positions && !rope_cos) return INFINI_ERR_ARG;
+  if (dims->dtype != INFINI_DTYPE_BF16 && dims->dtype != INFINI_DTYPE_F32) return INFINI_ERR_ARG;
+  if (dims->d_k != dims->d_v || !head_dim_ok(dims->d_k)) return INFINI_ERR_UNSUPPORTED;
+  const int d = dims->d_k;
+  const long long N = ((long long)dims->H_q + 2LL * dims->H_kv) * d;
+  const long long M = (long long)dims->B * dims->L;
+  W4Shape s;
+  int rc = w4_shape(N, d_model, group, &s);
+  if (rc != INFINI_OK) return rc;
+  if (M > 65535 * 64) return INFINI_ERR_UNSUPPORTED;
+  const size_t elem = dims->dtype == INFINI_DTYPE_BF16 ? 2 : 4;
+  const void* ptrs[] = {x, packed, scales, zeros, bias, rope_cos, rope_sin, positions, q, k, v};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return INFINI_ERR_ALIGN;
+  const size_t rot = rope_cos ? (size_t)n_pos * d / 2 * 4 : 0;
+  const Range ins[] = {rng(x, (size_t)M * d_model * elem), rng(packed, s.packed), rng(scales, s.scales),
+                       rng(zeros, zeros ? s.zeros : 0), rng(bias, bias ? (size_t)N * 4 : 0),
+                       rng(rope_cos, rot), rng(rope_sin, rot), rng(positions, positions ? (size_t)M * 4 : 0)};
+  const Range outs[] = {rng(q, (size_t)M * dims->H_q * d * elem), rng(k, (size_t)M * dims->H_kv * d * elem),
+                        rng(v, (size_t)M * dims->H_kv * d * elem)};
+  for (int i = 0; i < 3; ++i) {
+    for (const Range& r : ins)
+      if (overlap(outs[i], r)) return INFINI_ERR_ALIAS;
+    for (int j = i + 1; j < 3; ++j)
+      if (overlap(outs[i], outs[j])) return INFINI_ERR_ALIAS;
+  }
+  unsigned int* status = status_ptr();
+  if (!status) return INFINI_ERR_CUDA;
+  W4Problem p = {};
+  p.x = x; p.packed = static_cast<const uint8_t*>(packed);
+  p.scales = static_cast<const __nv_bfloat16*>(scales); p.zeros = static_cast<const uint8_t*>(zeros);
+  p.bias = bias; p.rope_cos = rope_cos; p.rope_sin = rope_sin; p.positions = positions; p.n_pos = n_pos;
+  p.q = q; p.k = k; p.v = v; p.M = (int)M; p.N = (int)N; p.K = d_model; p.group = group;
+  p.H_q = dims->H_q; p.H_kv = dims->H_kv; p.L = dims->L; p.d = d;
+  p.bf16 = dims->dtype == INFINI_DTYPE_BF16; p.status = status;
+  return w4_run(p, static_cast<cudaStream_t>(stream));
+}
+
 int infini_attn_sync_status(void* stream) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (cudaStreamSynchronize(st) != cudaSuccess) return INFINI_ERR_CUDA;
@@ -889,7 +1034,8 @@ int infini_attn_sync_status(void* stream) {
   if (word != 0) {
     const unsigned int zero = 0;
     if (cudaMemcpyToSymbol(g_status, &zero, sizeof(zero)) != cudaSuccess) return INFINI_ERR_CUDA;
-    return (word & infini::kStatusLayout) ? INFINI_ERR_UNSUPPORTED : INFINI_ERR_TIMEOUT;
+    if (word & infini::kStatusLayout) return INFINI_ERR_UNSUPPORTED;
+    return (word & infini::kStatusTimeout) ? INFINI_ERR_TIMEOUT : INFINI_ERR_RANGE;
   }
   return INFINI_OK;
 }

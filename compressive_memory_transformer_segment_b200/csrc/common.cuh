@@ -11,6 +11,7 @@ namespace infini {
 enum : unsigned int {
   kStatusTimeout = 1u,  // a bounded wait ran out
   kStatusLayout = 2u,   // a kernel found its shared memory not laid out as it requires
+  kStatusRange = 4u,    // a position read from device memory was out of its range
 };
 
 template <typename T> __device__ __forceinline__ float to_f32(T x);

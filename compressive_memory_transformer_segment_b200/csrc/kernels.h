@@ -1,6 +1,7 @@
 // Internal launcher declarations shared by the C-ABI layer and the kernels.
 #pragma once
 
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -164,6 +165,40 @@ bool block_norm_supported(int width);
 int block_norm_partials(long long rows, int width);
 cudaError_t launch_block_norm_forward(const BlockNormProblem& p, cudaStream_t stream);
 cudaError_t launch_block_norm_backward(const BlockNormProblem& p, cudaStream_t stream);
+
+// Projections of a few tokens with 4-bit weights.  packed [N][blocks][64]
+// bytes, blocks = ceil(K / 128); scales and zeros [N][blocks * 128 / group].
+struct W4Problem {
+  const void* x;                // [M][K]
+  const uint8_t* packed;
+  const __nv_bfloat16* scales;
+  const uint8_t* zeros;         // or null (8)
+  const float* bias;            // [N] or null
+  void* y;                      // [M][N], or null for the head projection:
+  const float* rope_cos;        // [n_pos][d / 2] or null
+  const float* rope_sin;
+  const int* positions;         // [M] or null (token l of its batch row: l)
+  void* q;                      // [B, H_q, L, d]
+  void* k;                      // [B, H_kv, L, d]
+  void* v;
+  int M, N, K, group;
+  int H_q, H_kv, L, d, n_pos;
+  bool bf16;
+  unsigned int* status;
+};
+cudaError_t launch_w4(const W4Problem& p, cudaStream_t stream);
+// Quantise w [N][K] (bf16 or fp32) into packed, scales and zeros; pack codes
+// (w: uint8 [N][K]); dequantise into w.
+struct W4PackProblem {
+  const void* w;
+  uint8_t* packed;
+  __nv_bfloat16* scales;
+  uint8_t* zeros;               // or null
+  int N, K, group;
+  bool bf16;
+};
+enum class W4Layout { kQuantize, kPack, kDequantize };
+cudaError_t launch_w4_layout(const W4PackProblem& p, W4Layout what, cudaStream_t stream);
 
 int decode_splits(int S);
 int decode_head_chunks(int g);

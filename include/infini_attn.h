@@ -76,7 +76,8 @@ typedef enum {
   INFINI_ERR_TIMEOUT = -5,      /* a kernel gave up waiting (device-side)   */
   INFINI_ERR_WORKSPACE = -6,    /* workspace too small or misaligned        */
   INFINI_ERR_ALIGN = -7,        /* a pointer is not 16-byte aligned         */
-  INFINI_ERR_SCRATCH_LIMIT = -8 /* problem too large for infini_attn_forward_noalloc */
+  INFINI_ERR_SCRATCH_LIMIT = -8, /* problem too large for infini_attn_forward_noalloc */
+  INFINI_ERR_RANGE = -9         /* a position in device memory was out of range (device-side) */
 } infini_status_t;
 
 /* Problem sizes.  Layouts (all contiguous, row-major):
@@ -291,6 +292,71 @@ INFINI_API int infini_attn_qkv_project(const void* x, const void* w_qkv, const f
 INFINI_API int infini_attn_rope_tables(float* cos_out, float* sin_out, int n_pos, int d,
                                        double base, void* stream);
 
+/* Weights in 4 bits, for projections of one or a few tokens.
+ *
+ * A matrix [N, K] is held as codes q in 0..15 with a bf16 scale and, if
+ * given, a zero point in 0..15 (8 otherwise) for each group of `group`
+ * consecutive channels of a row:
+ *   w[n][k] = scales[n][k / group] (q[n][k] - zeros[n][k / group])
+ *   packed     device [N, blocks, 64] bytes, blocks = ceil(K / 128): a block
+ *              holds 128 channels as 16 little-endian 32-bit words; word
+ *              4 c + j (c, j = 0..3) holds channels 32 j + 8 c + o, o = 0..7,
+ *              with even o in bits 2 o .. 2 o + 3 and odd o in bits
+ *              2 o + 14 .. 2 o + 17.  Codes of channels >= K are ignored.
+ *   scales     device bf16 [N, blocks * 128 / group]; finite.  Groups without
+ *              a channel < K are ignored.
+ *   zeros      device uint8, the shape of scales, values 0..15, or NULL
+ *   group      32, 64 or 128
+ * K must be a multiple of 8 (INFINI_ERR_UNSUPPORTED).
+ *
+ * infini_attn_w4_quantize rounds w [N, K] (element type dtype, finite) to the
+ * nearest codes: with zeros, scale = bf16(range / 15) of the group's values
+ * and 0, zero = round(-low / scale); without, scale = bf16(max |w| / 7).
+ * infini_attn_w4_pack lays out codes a caller has (uint8 [N, K]; bits above
+ * the lowest four are dropped).  infini_attn_w4_dequantize writes w [N, K].
+ * All device pointers, 16-byte aligned; outputs overlap nothing; asynchronous
+ * on `stream`.  Errors: INFINI_ERR_ARG, _UNSUPPORTED, _ALIGN, _ALIAS, _CUDA. */
+INFINI_API int infini_attn_w4_quantize(const void* w, int N, int K, int group, int dtype, void* packed,
+                                       void* scales, void* zeros, void* stream);
+INFINI_API int infini_attn_w4_pack(const void* codes, int N, int K, void* packed, void* stream);
+INFINI_API int infini_attn_w4_dequantize(const void* packed, const void* scales, const void* zeros,
+                                         int N, int K, int group, int dtype, void* w, void* stream);
+
+/* y[t] = W x[t] + bias for M tokens, W in 4 bits as above:
+ *   x          device [M, K], element type dtype (finite)
+ *   bias       device float32 [N] or NULL
+ *   y          device [M, N], element type dtype; overlaps no input
+ *   stream     cudaStream_t; asynchronous, no workspace.
+ * Group sums are taken over the exact integers q - zero and scaled in fp32;
+ * the result is rounded once.  Made for few tokens: the weights are read once
+ * for every 64.  Supported: M <= 4194240.  Repeated calls are bitwise equal, and a
+ * token's result does not depend on the values of the other tokens. */
+INFINI_API int infini_attn_linear_w4(const void* x, const void* packed, const void* scales,
+                                     const void* zeros, const float* bias, int M, int N, int K,
+                                     int group, int dtype, void* y, void* stream);
+
+/* infini_attn_qkv_project with W in 4 bits, N = (H_q + 2 H_kv) d rows, for
+ * the B * L tokens of a decode step (L = 1) or a short run of tokens.
+ *   x          device [B, L, d_model], element type dims->dtype
+ *   bias, rope_cos, rope_sin
+ *              as for infini_attn_qkv_project, but the tables have n_pos rows
+ *   n_pos      rows of the tables; >= L if positions is NULL
+ *   positions  device int32 [B, L], the table row of each token, or NULL
+ *              (token t of every batch row uses row t); needs the tables.  A
+ *              value outside [0, n_pos) is reported by
+ *              infini_attn_sync_status (INFINI_ERR_RANGE) and the token's
+ *              heads are not rotated.
+ *   dims       B, H_q, H_kv, L, d_k = d_v = d in {32, 64, 128}, dtype
+ *   q, k, v    device [B, H_q, L, d], [B, H_kv, L, d], [B, H_kv, L, d],
+ *              element type dims->dtype
+ * Errors: those of infini_attn_linear_w4 and infini_attn_qkv_project. */
+INFINI_API int infini_attn_qkv_project_w4(const void* x, const void* packed, const void* scales,
+                                          const void* zeros, const float* bias,
+                                          const float* rope_cos, const float* rope_sin, int n_pos,
+                                          const int* positions, const infini_dims_t* dims,
+                                          int d_model, int group, void* q, void* k, void* v,
+                                          void* stream);
+
 /* Norms before and after the layer, fused with the block's gate, residual
  * scale and residual sum.  The reproduction trains Llama models ("Hugging Face
  * Infini-Attention 再現分析"), whose layers read a root-mean-square norm of the
@@ -440,8 +506,9 @@ INFINI_API int infini_attn_forward_host(const void* q_h, const void* k_h, const 
  * the kernels set when one of their bounded waits ran out:
  * INFINI_OK, INFINI_ERR_TIMEOUT, INFINI_ERR_UNSUPPORTED if a kernel found
  * its dynamic shared memory placed where its layout cannot use it (it then
- * computes nothing), or INFINI_ERR_CUDA if the stream itself reported an
- * error. */
+ * computes nothing), INFINI_ERR_RANGE if a kernel read a position outside its
+ * range from device memory (each such call says what it then did), or
+ * INFINI_ERR_CUDA if the stream itself reported an error. */
 INFINI_API int infini_attn_sync_status(void* stream);
 
 /* Benchmark support: per-kernel device timing.  While enabled, every

@@ -25,6 +25,9 @@ form of the rotation and its invariants.
 The norms around the layer (``infini_block_norm``: block_norm,
 block_norm_vjp) are pinned in ``tests/test_oracle_block_norm.py`` against loops
 over single elements and central finite differences.
+The 4-bit weights and segment buffer (``infini_4bit``) are pinned in
+``tests/test_oracle_4bit.py`` against bit-string packing, bounds of the
+rounding and the layer oracle's own forward.
 No function here is "parity unpinned".
 """
 
@@ -57,4 +60,15 @@ from .infini_projection import (  # noqa: F401
 from .infini_block_norm import (  # noqa: F401
     block_norm,
     block_norm_vjp,
+)
+from .infini_4bit import (  # noqa: F401
+    bf16,
+    cache_codes,
+    cache_values,
+    codes_of,
+    decode_step_q4,
+    key_bit,
+    packed_of,
+    value_bit,
+    w4_weight,
 )

@@ -304,6 +304,61 @@ def test_block_norm_checks_arguments_on_the_host(lib):
     assert back(ws=bwd["dr"]) == api.ERR_ALIAS
 
 
+def test_w4_checks_arguments_on_the_host(lib):
+    """Argument checks of the 4-bit projections return before any CUDA call."""
+    MB = 1 << 20
+    good = dict(x=1 * MB, packed=2 * MB, scales=4 * MB, zeros=5 * MB, bias=6 * MB, M=4, N=256, K=512,
+                group=64, dtype=0, y=8 * MB)
+
+    def call(**over):
+        return lib.infini_attn_linear_w4(*dict(good, **over).values(), None)
+
+    for name in ("x", "packed", "scales", "y"):
+        assert call(**{name: None}) == api.ERR_ARG
+    for name in ("M", "N", "K", "group"):
+        assert call(**{name: 0}) == api.ERR_ARG
+    assert call(dtype=3) == api.ERR_ARG
+    assert call(K=516) == api.ERR_UNSUPPORTED
+    assert call(group=16) == api.ERR_UNSUPPORTED
+    assert call(M=65535 * 64 + 1) == api.ERR_UNSUPPORTED
+    assert call(N=0x7fffffff) == api.ERR_UNSUPPORTED
+    assert call(zeros=5 * MB + 2) == api.ERR_ALIGN
+    assert call(y=good["x"]) == api.ERR_ALIAS
+    assert call(y=good["packed"] + 64) == api.ERR_ALIAS
+
+    dims = api.make_dims(2, 4, 2, 3, 64, 64, 0)
+    proj = dict(x=1 * MB, packed=2 * MB, scales=4 * MB, zeros=None, bias=None, cos=6 * MB, sin=7 * MB,
+                n_pos=16, positions=9 * MB, dims=ctypes.byref(dims), d_model=256, group=128, q=10 * MB,
+                k=11 * MB, v=12 * MB)
+
+    def qkv(**over):
+        return lib.infini_attn_qkv_project_w4(*dict(proj, **over).values(), None)
+
+    for name in ("x", "packed", "scales", "q", "k", "v", "sin"):
+        assert qkv(**{name: None}) == api.ERR_ARG
+    assert qkv(n_pos=0) == api.ERR_ARG
+    assert qkv(positions=None, n_pos=2) == api.ERR_ARG       # fewer table rows than tokens
+    assert qkv(cos=None, sin=None) == api.ERR_ARG            # positions without tables
+    assert qkv(dims=ctypes.byref(api.make_dims(2, 4, 2, 3, 64, 32, 0))) == api.ERR_UNSUPPORTED
+    assert qkv(dims=ctypes.byref(api.make_dims(2, 4, 2, 3, 48, 48, 0))) == api.ERR_UNSUPPORTED
+    assert qkv(dims=ctypes.byref(api.make_dims(1 << 12, 4, 2, 1 << 12, 64, 64, 0))) == api.ERR_UNSUPPORTED
+    assert qkv(dims=ctypes.byref(api.make_dims(1, 1 << 25, 1, 1, 64, 64, 0))) == api.ERR_UNSUPPORTED
+    assert qkv(d_model=12) == api.ERR_UNSUPPORTED
+    assert qkv(q=10 * MB + 4) == api.ERR_ALIGN
+    assert qkv(k=proj["v"] + 16) == api.ERR_ALIAS
+    assert qkv(q=proj["positions"]) == api.ERR_ALIAS
+
+    assert lib.infini_attn_w4_quantize(None, 4, 64, 32, 0, MB, 2 * MB, None, None) == api.ERR_ARG
+    assert lib.infini_attn_w4_quantize(MB, 4, 60, 32, 0, 2 * MB, 3 * MB, None, None) == api.ERR_UNSUPPORTED
+    assert lib.infini_attn_w4_quantize(MB, 4, 64, 48, 0, 2 * MB, 3 * MB, None, None) == api.ERR_UNSUPPORTED
+    assert lib.infini_attn_w4_quantize(MB, 4, 64, 32, 0, MB + 64, 3 * MB, None, None) == api.ERR_ALIAS
+    assert lib.infini_attn_w4_pack(MB, 4, 64, None, None) == api.ERR_ARG
+    assert lib.infini_attn_w4_pack(MB, 0, 64, 2 * MB, None) == api.ERR_ARG
+    assert lib.infini_attn_w4_dequantize(MB, 2 * MB, None, 4, 64, 32, 1, MB, None) == api.ERR_ALIAS
+    assert lib.infini_attn_w4_dequantize(MB, 2 * MB, None, 4, 64, 32, 7, 3 * MB, None) == api.ERR_ARG
+    assert api.status_string(api.ERR_RANGE) != api.status_string(12345)
+
+
 def test_plain_c_program_uses_the_boundary(tmp_path):
     """The header compiles as C99 and a C program linked against the library
     gets the documented answers from the host-side calls (no GPU needed)."""
