@@ -39,6 +39,10 @@ class Plan(ctypes.Structure):
                 ("num_segments", ctypes.c_int), ("workspace_bytes", ctypes.c_size_t)]
 
 
+class _CacheQ4Ptrs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_codes", "k_scale", "v_codes", "v_scale")]
+
+
 class InfiniError(RuntimeError):
     def __init__(self, status, message):
         super().__init__(f"infini_attn status {status}: {message}")
@@ -103,6 +107,19 @@ _SIGNATURES = [
     ("infini_attn_linear_w4", ctypes.c_int, [_P] * 5 + [ctypes.c_int] * 5 + [_P] * 2),
     ("infini_attn_qkv_project_w4", ctypes.c_int, [_P] * 7 + [ctypes.c_int, _P, ctypes.POINTER(Dims),
                                                              ctypes.c_int, ctypes.c_int] + [_P] * 4),
+    ("infini_attn_cache_q4_append", ctypes.c_int, [_P, _P, _P, ctypes.POINTER(Dims), ctypes.c_int,
+                                                   ctypes.POINTER(_CacheQ4Ptrs), _P]),
+    ("infini_attn_cache_q4_read", ctypes.c_int, [ctypes.POINTER(_CacheQ4Ptrs), ctypes.POINTER(Dims),
+                                                 ctypes.c_int, _P, _P, _P]),
+    ("infini_attn_state_update_q4_workspace_bytes", ctypes.c_size_t, [ctypes.POINTER(Dims),
+                                                                      ctypes.c_int]),
+    ("infini_attn_state_update_q4", ctypes.c_int, [ctypes.POINTER(_CacheQ4Ptrs), _P, _P, ctypes.c_int,
+                                                   ctypes.POINTER(Dims), ctypes.c_int, _P, _P, _P,
+                                                   ctypes.c_size_t, _P]),
+    ("infini_attn_decode_q4_workspace_bytes", ctypes.c_size_t, [ctypes.POINTER(Dims), ctypes.c_int]),
+    ("infini_attn_decode_step_q4", ctypes.c_int, [_P, _P, _P, _P, ctypes.POINTER(_CacheQ4Ptrs), _P, _P,
+                                                  _P, ctypes.c_int, ctypes.POINTER(Dims), _P, _P,
+                                                  ctypes.c_size_t, _P]),
     ("infini_attn_backward", ctypes.c_int, [_P, _P, _P, _P, _P, _P, ctypes.c_int, ctypes.c_int,
                                             ctypes.POINTER(Dims), _P, _P, _P, _P, _P, _P, _P, _P,
                                             _P, _P, ctypes.c_size_t, _P]),
@@ -420,6 +437,14 @@ def _cuda_device(t, name):
     return t.device
 
 
+def _workspace(t, dev):
+    """(address, bytes) of an optional workspace tensor."""
+    if t is None:
+        return None, 0
+    n = t.numel()
+    return _arg(t, "workspace", torch.uint8, (n,), dev), n
+
+
 def _empty(shape, dtype, dev, stream):
     """New memory for an output that ``stream`` writes: of that stream's pool."""
     if stream is None:
@@ -508,9 +533,7 @@ def block_norm_backward(dr_out, dh, r_out, rstd_next, w_next, o=None, gate=None,
     dgate = _empty(shape, dt, dev, stream) if gate is not None else None
     dscale, dw_post, dw_next = (_empty(vec, f32, dev, stream) if w is not None else None
                                 for w in (scale, w_post, w_next))
-    ws, ws_n = None, 0
-    if workspace is not None:
-        ws, ws_n = _arg(workspace, "workspace", torch.uint8, (workspace.numel(),), dev), workspace.numel()
+    ws, ws_n = _workspace(workspace, dev)
     _call(load_library().infini_attn_block_norm_backward, dev, stream,
           _arg(dr_out, "dr_out", dt, shape, dev), _arg(dh, "dh", dt, shape, dev),
           _arg(r_out, "r_out", dt, shape, dev), _arg(o, "o", dt, shape, dev),
@@ -700,6 +723,164 @@ class DecodeStream:
         n = self.pos
         return state_update(self.k_buf[:, :, :n].contiguous(), self.v_buf[:, :, :n].contiguous(),
                             self.M, self.z, n, self.rule, stream=stream)
+
+
+class CacheQ4:
+    """A segment buffer in 4 bits (see infini_cache_q4_t): codes uint8
+    [B, H_kv, S, d / 2] and scales bfloat16 [B, H_kv, S, d / 32, 2] of the keys
+    and the values.  The tensors are checked once, here; the object keeps
+    them."""
+
+    def __init__(self, k_codes, k_scale, v_codes, v_scale):
+        dev = self.device = _cuda_device(k_codes, "k_codes")
+        if k_codes.dim() != 4:
+            raise ValueError("k_codes must be [B, H_kv, S, d / 2]")
+        B, H, S, half = k_codes.shape
+        self.B, self.H_kv, self.seg_len, self.d = B, H, S, 2 * half
+        if self.d not in (32, 64, 128) or S < 1:
+            raise ValueError("the buffer's rows must hold 32, 64 or 128 channels")
+        scale = (B, H, S, self.d // 32, 2)
+        self.tensors = (k_codes, k_scale, v_codes, v_scale)
+        self._ptrs = _CacheQ4Ptrs(_arg(k_codes, "k_codes", torch.uint8, k_codes.shape, dev),
+                                  _arg(k_scale, "k_scale", torch.bfloat16, scale, dev),
+                                  _arg(v_codes, "v_codes", torch.uint8, k_codes.shape, dev),
+                                  _arg(v_scale, "v_scale", torch.bfloat16, scale, dev))
+        self._ref = ctypes.byref(self._ptrs)
+        self._dims = {}  # per (H_q, L, dtype): the struct the calls take
+        self._lib = load_library()
+
+    @classmethod
+    def empty(cls, B, H_kv, seg_len, d, device=None):
+        """A new buffer (zeros: every row reads as 0)."""
+        device = device or torch.device("cuda", torch.cuda.current_device())
+        codes = (B, H_kv, seg_len, d // 2)
+        scale = (B, H_kv, seg_len, d // 32, 2)
+        return cls(torch.zeros(codes, dtype=torch.uint8, device=device),
+                   torch.zeros(scale, dtype=torch.bfloat16, device=device),
+                   torch.zeros(codes, dtype=torch.uint8, device=device),
+                   torch.zeros(scale, dtype=torch.bfloat16, device=device))
+
+    def row(self, b):
+        """Batch row b alone, as a view."""
+        return CacheQ4(*(t[b:b + 1] for t in self.tensors))
+
+    def _dims_ref(self, H_q, L, dtype):
+        key = (H_q, L, dtype)
+        ref = self._dims.get(key)
+        if ref is None:
+            if dtype not in DTYPES:
+                raise ValueError("dtype must be bfloat16 or float32")
+            ref = ctypes.byref(Dims(self.B, H_q, self.H_kv, L, self.d, self.d, DTYPES[dtype]))
+            if len(self._dims) > 64:
+                self._dims.clear()
+            self._dims[key] = ref
+        return ref
+
+    def append(self, k, v, pos, stream=None):
+        """infini_attn_cache_q4_append: k, v [B, H_kv, n, d] (bfloat16 or
+        float32) into rows pos[b] .. pos[b] + n - 1, pos int32 [B]."""
+        dev, dt, shape = self.device, k.dtype, k.shape
+        if k.dim() != 4 or shape != (self.B, self.H_kv, shape[2], self.d):
+            raise ValueError(f"k must be [{self.B}, {self.H_kv}, n, {self.d}]")
+        _call(self._lib.infini_attn_cache_q4_append, dev, stream, _arg(k, "k", dt, shape, dev),
+              _arg(v, "v", dt, shape, dev), _arg(pos, "pos", torch.int32, (self.B,), dev),
+              self._dims_ref(self.H_kv, shape[2], dt), self.seg_len, self._ref)
+
+    def read(self, n, dtype=torch.float32, k=None, v=None, stream=None):
+        """infini_attn_cache_q4_read: the values of rows 0 .. n - 1, as
+        (k, v) [B, H_kv, n, d]."""
+        dev, shape = self.device, (self.B, self.H_kv, int(n), self.d)
+        dims = self._dims_ref(self.H_kv, int(n), dtype)
+        k = _empty(shape, dtype, dev, stream) if k is None else k
+        v = _empty(shape, dtype, dev, stream) if v is None else v
+        _call(self._lib.infini_attn_cache_q4_read, dev, stream, self._ref, dims, self.seg_len,
+              _arg(k, "k", dtype, shape, dev), _arg(v, "v", dtype, shape, dev))
+        return k, v
+
+    def state_update(self, n, M_in, z_in, rule, dtype=torch.bfloat16, M_out=None, z_out=None,
+                     workspace=None, stream=None):
+        """infini_attn_state_update_q4: the memory after the first n rows as
+        one segment; returns (M_out, z_out), which may be (M_in, z_in)."""
+        dev, f32 = self.device, torch.float32
+        ms, zs = (self.B, self.H_kv, self.d, self.d), (self.B, self.H_kv, self.d)
+        dims = self._dims_ref(self.H_kv, int(n), dtype)
+        M_out = _empty(ms, f32, dev, stream) if M_out is None else M_out
+        z_out = _empty(zs, f32, dev, stream) if z_out is None else z_out
+        ws, ws_n = _workspace(workspace, dev)
+        _call(self._lib.infini_attn_state_update_q4, dev, stream, self._ref, _arg(M_in, "M_in", f32, ms, dev),
+              _arg(z_in, "z_in", f32, zs, dev), _rule(rule), dims, self.seg_len,
+              _arg(M_out, "M_out", f32, ms, dev), _arg(z_out, "z_out", f32, zs, dev), ws, ws_n)
+        return M_out, z_out
+
+
+def state_update_q4_workspace_bytes(B, H_kv, n, d, rule, dtype=torch.bfloat16):
+    dims = make_dims(B, H_kv, H_kv, n, d, d, dtype)
+    return load_library().infini_attn_state_update_q4_workspace_bytes(ctypes.byref(dims), _rule(rule))
+
+
+def decode_q4_workspace_bytes(B, H_q, H_kv, seg_len, d):
+    """infini_attn_decode_q4_workspace_bytes (0 for unsupported sizes)."""
+    dims = make_dims(B, H_q, H_kv, 1, d, d, 0)
+    return load_library().infini_attn_decode_q4_workspace_bytes(ctypes.byref(dims), int(seg_len))
+
+
+def decode_step_q4(q_t, k_t, v_t, beta, cache, pos, M, z, out=None, workspace=None, stream=None):
+    """infini_attn_decode_step_q4: q_t [B, H_q, d], k_t, v_t [B, H_kv, d]
+    (bfloat16 or float32), ``cache`` a CacheQ4, pos int32 [B] (-1: idle), M, z
+    the memory before the segment (read only).  ``workspace``: a uint8 tensor
+    of decode_q4_workspace_bytes(...), zero-filled before its first step.
+    Returns out [B, H_q, d]; idle rows of an ``out`` that is given keep what
+    they hold, and are undefined in one that is not."""
+    dev, dt, shape, f32 = cache.device, q_t.dtype, q_t.shape, torch.float32
+    B, H, d = cache.B, cache.H_kv, cache.d
+    if q_t.dim() != 3 or shape != (B, shape[1], d):
+        raise ValueError(f"q_t must be [{B}, H_q, {d}]")
+    tok = (B, H, d)
+    dims = cache._dims_ref(shape[1], 1, dt)
+    if out is None:
+        out = _empty(shape, dt, dev, stream)
+    ws, ws_n = _workspace(workspace, dev)
+    _call(cache._lib.infini_attn_decode_step_q4, dev, stream, _arg(q_t, "q_t", dt, shape, dev),
+          _arg(k_t, "k_t", dt, tok, dev), _arg(v_t, "v_t", dt, tok, dev),
+          _arg(beta, "beta", f32, (shape[1],), dev), cache._ref, _arg(pos, "pos", torch.int32, (B,), dev),
+          _arg(M, "M", f32, (B, H, d, d), dev), _arg(z, "z", f32, tok, dev), cache.seg_len, dims,
+          _arg(out, "out", dt, shape, dev), ws, ws_n)
+    return out
+
+
+class DecodeStreamQ4:
+    """DecodeStream with its segment buffer in 4 bits: one token per step for
+    every stream, all at the same position (marshalling around decode_step_q4
+    and CacheQ4.state_update)."""
+
+    def __init__(self, B, H_q, H_kv, d, seg_len, rule, dtype=torch.bfloat16, device=None, M=None, z=None):
+        device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        self.seg_len, self.rule, self.pos, self.dtype = int(seg_len), rule, 0, dtype
+        self.cache = CacheQ4.empty(B, H_kv, self.seg_len, d, device)
+        f32 = dict(dtype=torch.float32, device=device)
+        self.M = torch.zeros((B, H_kv, d, d), **f32) if M is None else M.clone()
+        self.z = torch.zeros((B, H_kv, d), **f32) if z is None else z.clone()
+        self._pos = torch.zeros(B, dtype=torch.int32, device=device)
+        # zero-filled: the step's ticket counters start at 0
+        self.workspace = torch.zeros(decode_q4_workspace_bytes(B, H_q, H_kv, self.seg_len, d),
+                                     dtype=torch.uint8, device=device)
+
+    def step(self, q_t, k_t, v_t, beta, out=None):
+        self._pos.fill_(self.pos)
+        out = decode_step_q4(q_t, k_t, v_t, beta, self.cache, self._pos, self.M, self.z, out=out,
+                             workspace=self.workspace)
+        self.pos += 1
+        if self.pos == self.seg_len:
+            self.cache.state_update(self.seg_len, self.M, self.z, self.rule, self.dtype, self.M, self.z)
+            self.pos = 0
+        return out
+
+    def final_state(self):
+        """(M, z) after every token so far, counting a partly filled segment
+        (the stream itself is left unchanged)."""
+        if self.pos == 0:
+            return self.M.clone(), self.z.clone()
+        return self.cache.state_update(self.pos, self.M, self.z, self.rule, self.dtype)
 
 
 def host_arena_bytes(dims, seg_len, rule):

@@ -16,7 +16,8 @@ NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 SOURCES = ["api.cu", "simt.cu", "tc_attention.cu", "tc_attention_single.cu", "tc_attention_small.cu",
            "tc_scan.cu", "selftest.cu", "noalloc.cu", "decode.cu", "backward.cu",
-           "qkv_rope.cu", "block_norm.cu", "w4.cu"]
+           "qkv_rope.cu", "block_norm.cu", "w4.cu",
+           "q4_decode.cu"]
 FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17",

@@ -1026,6 +1026,234 @@ int infini_attn_qkv_project_w4(const void* x, const void* packed, const void* sc
   return w4_run(p, static_cast<cudaStream_t>(stream));
 }
 
+namespace {
+
+// A segment buffer in 4 bits: its four arrays, checked and as ranges.
+struct CacheQ4 {
+  uint8_t* k_codes;
+  __nv_bfloat16* k_scale;
+  uint8_t* v_codes;
+  __nv_bfloat16* v_scale;
+  Range r[4];
+};
+
+// Sizes and pointers shared by the calls on a 4-bit segment buffer.
+int q4_shape(const infini_dims_t* d, int seg_len, const infini_cache_q4_t* cache, CacheQ4* c) {
+  if (!d || d->B < 1 || d->H_kv < 1 || seg_len < 1) return INFINI_ERR_ARG;
+  if (d->dtype != INFINI_DTYPE_BF16 && d->dtype != INFINI_DTYPE_F32) return INFINI_ERR_ARG;
+  if (d->d_k != d->d_v || !head_dim_ok(d->d_k) || (long long)d->B * d->H_kv > 65535 || seg_len > (1 << 30))
+    return INFINI_ERR_UNSUPPORTED;
+  if (!cache || !cache->k_codes || !cache->k_scale || !cache->v_codes || !cache->v_scale) return INFINI_ERR_ARG;
+  const size_t rows = (size_t)d->B * d->H_kv * seg_len;
+  const size_t codes = rows * (d->d_k / 2), scale = rows * (d->d_k / 32) * 4;
+  void* const ptrs[] = {cache->k_codes, cache->k_scale, cache->v_codes, cache->v_scale};
+  for (int i = 0; i < 4; ++i) {
+    if (!aligned16(ptrs[i])) return INFINI_ERR_ALIGN;
+    c->r[i] = rng(ptrs[i], i % 2 == 0 ? codes : scale);
+    for (int j = 0; j < i; ++j)
+      if (overlap(c->r[i], c->r[j])) return INFINI_ERR_ALIAS;
+  }
+  c->k_codes = static_cast<uint8_t*>(cache->k_codes);
+  c->k_scale = static_cast<__nv_bfloat16*>(cache->k_scale);
+  c->v_codes = static_cast<uint8_t*>(cache->v_codes);
+  c->v_scale = static_cast<__nv_bfloat16*>(cache->v_scale);
+  return INFINI_OK;
+}
+
+Q4Problem q4_problem(const infini_dims_t* d, int seg_len, const CacheQ4& c) {
+  Q4Problem p = {};
+  p.k_codes = c.k_codes; p.k_scale = c.k_scale; p.v_codes = c.v_codes; p.v_scale = c.v_scale;
+  p.B = d->B; p.H_q = d->H_q; p.H_kv = d->H_kv; p.d = d->d_k; p.S = seg_len;
+  p.bf16 = d->dtype == INFINI_DTYPE_BF16;
+  return p;
+}
+
+// Workspace of a 4-bit decode step: [tickets | attention partials | retrieval].
+struct Q4Layout {
+  int chunk, nsplit;
+  size_t part, ret, total;
+};
+
+int q4_layout(const infini_dims_t* d, int seg_len, Q4Layout* lay) {
+  if (!d || d->B < 1 || d->H_q < 1 || d->H_kv < 1 || seg_len < 1 || d->H_q % d->H_kv != 0)
+    return INFINI_ERR_ARG;
+  if (d->d_k != d->d_v || !head_dim_ok(d->d_k) || (long long)d->B * d->H_q > 65535 || seg_len > (1 << 30))
+    return INFINI_ERR_UNSUPPORTED;
+  const int zc = q4_head_chunks(d->H_q / d->H_kv);
+  const size_t BHq = (size_t)d->B * d->H_q, dd = d->d_k;
+  lay->chunk = q4_chunk_rows((long long)d->B * d->H_kv * zc, seg_len);
+  lay->nsplit = (seg_len + lay->chunk - 1) / lay->chunk;
+  lay->part = align_up((size_t)d->B * d->H_kv * zc * 4);
+  lay->ret = align_up(lay->part + BHq * lay->nsplit * (dd + 2) * 4);
+  lay->total = align_up(lay->ret + BHq * (dd + 1) * 4);
+  return INFINI_OK;
+}
+
+}  // namespace
+
+int infini_attn_cache_q4_append(const void* k, const void* v, const int* pos, const infini_dims_t* dims,
+                                int seg_len, const infini_cache_q4_t* cache, void* stream) {
+  CacheQ4 c;
+  int rc = q4_shape(dims, seg_len, cache, &c);
+  if (rc != INFINI_OK) return rc;
+  if (!k || !v || !pos || dims->L < 1) return INFINI_ERR_ARG;
+  if (dims->L > seg_len) return INFINI_ERR_ARG;
+  const void* ptrs[] = {k, v, pos};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return INFINI_ERR_ALIGN;
+  const size_t n = (size_t)dims->B * dims->H_kv * dims->L * dims->d_k *
+                   (dims->dtype == INFINI_DTYPE_BF16 ? 2 : 4);
+  const Range ins[] = {rng(k, n), rng(v, n), rng(pos, (size_t)dims->B * 4)};
+  for (const Range& r : c.r)
+    for (const Range& in : ins)
+      if (overlap(r, in)) return INFINI_ERR_ALIAS;
+  Q4Problem p = q4_problem(dims, seg_len, c);
+  p.k_t = k; p.v_t = v; p.pos = pos;
+  p.status = status_ptr();
+  if (!p.status) return INFINI_ERR_CUDA;
+  return launch_q4(p, Q4What::kAppend, dims->L, nullptr, nullptr, static_cast<cudaStream_t>(stream)) ==
+                 cudaSuccess
+             ? INFINI_OK
+             : INFINI_ERR_CUDA;
+}
+
+int infini_attn_cache_q4_read(const infini_cache_q4_t* cache, const infini_dims_t* dims, int seg_len,
+                              void* k, void* v, void* stream) {
+  CacheQ4 c;
+  int rc = q4_shape(dims, seg_len, cache, &c);
+  if (rc != INFINI_OK) return rc;
+  if (!k || !v || dims->L < 1 || dims->L > seg_len) return INFINI_ERR_ARG;
+  if (!aligned16(k) || !aligned16(v)) return INFINI_ERR_ALIGN;
+  const size_t n = (size_t)dims->B * dims->H_kv * dims->L * dims->d_k *
+                   (dims->dtype == INFINI_DTYPE_BF16 ? 2 : 4);
+  if (overlap(rng(k, n), rng(v, n))) return INFINI_ERR_ALIAS;
+  for (const Range& r : c.r)
+    if (overlap(r, rng(k, n)) || overlap(r, rng(v, n))) return INFINI_ERR_ALIAS;
+  return launch_q4(q4_problem(dims, seg_len, c), Q4What::kRead, dims->L, k, v,
+                   static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? INFINI_OK
+             : INFINI_ERR_CUDA;
+}
+
+size_t infini_attn_state_update_q4_workspace_bytes(const infini_dims_t* dims, int rule) {
+  Shape s;
+  if (!dims) return 0;
+  infini_dims_t one = *dims;
+  one.H_q = one.H_kv;
+  if (check_shape(&one, one.L, rule, &s) != INFINI_OK || s.d_k != s.d_v) return 0;
+  return align_up(s.k_bytes) + align_up(s.v_bytes) + s.ws_total;
+}
+
+int infini_attn_state_update_q4(const infini_cache_q4_t* cache, const float* M_in, const float* z_in,
+                                int rule, const infini_dims_t* dims, int seg_len, float* M_out,
+                                float* z_out, void* workspace, size_t workspace_bytes, void* stream) {
+  CacheQ4 c;
+  int rc = q4_shape(dims, seg_len, cache, &c);
+  if (rc != INFINI_OK) return rc;
+  if (!M_in || !z_in || !M_out || !z_out || dims->L < 1 || dims->L > seg_len) return INFINI_ERR_ARG;
+  Shape s;
+  infini_dims_t one = *dims;
+  one.H_q = one.H_kv;
+  rc = check_shape(&one, one.L, rule, &s);  // one segment of L rows
+  if (rc != INFINI_OK) return rc;
+  const size_t total = infini_attn_state_update_q4_workspace_bytes(dims, rule);
+  const void* ptrs[] = {M_in, z_in, M_out, z_out};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return INFINI_ERR_ALIGN;
+  if (workspace == nullptr && workspace_bytes != 0) return INFINI_ERR_ARG;
+  if (workspace && (workspace_bytes < total || ((uintptr_t)workspace & (kAlign - 1)) != 0))
+    return INFINI_ERR_WORKSPACE;
+  const Range r_M = rng(M_out, s.M_bytes), r_z = rng(z_out, s.z_bytes), r_ws = rng(workspace, workspace ? total : 0);
+  const Range ins[] = {rng(M_in, s.M_bytes), rng(z_in, s.z_bytes), c.r[0], c.r[1], c.r[2], c.r[3]};
+  for (int i = 0; i < 6; ++i) {
+    if (overlap(r_M, ins[i]) && !(i == 0 && M_out == M_in)) return INFINI_ERR_ALIAS;
+    if (overlap(r_z, ins[i]) && !(i == 1 && z_out == z_in)) return INFINI_ERR_ALIAS;
+    if (overlap(r_ws, ins[i])) return INFINI_ERR_ALIAS;
+  }
+  if (overlap(r_M, r_z) || overlap(r_ws, r_M) || overlap(r_ws, r_z)) return INFINI_ERR_ALIAS;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  unsigned int* status = status_ptr();
+  if (!status) return INFINI_ERR_CUDA;
+  char* ws = static_cast<char*>(workspace);
+  bool owned = false;
+  if (!ws) {
+    if (cudaMallocAsync(reinterpret_cast<void**>(&ws), total, st) != cudaSuccess) return INFINI_ERR_CUDA;
+    owned = true;
+  }
+  void* k = ws;
+  void* v = ws + align_up(s.k_bytes);
+  cudaError_t e = launch_q4(q4_problem(dims, seg_len, c), Q4What::kRead, dims->L, k, v, st);
+  if (e == cudaSuccess)
+    e = run_state_scan(s, k, v, M_in, z_in, M_out, z_out, ws + align_up(s.k_bytes) + align_up(s.v_bytes),
+                       status, st);
+  if (owned) {
+    cudaError_t f = cudaFreeAsync(ws, st);
+    if (e == cudaSuccess) e = f;
+  }
+  return e == cudaSuccess ? INFINI_OK : INFINI_ERR_CUDA;
+}
+
+size_t infini_attn_decode_q4_workspace_bytes(const infini_dims_t* dims, int seg_len) {
+  Q4Layout lay;
+  return q4_layout(dims, seg_len, &lay) == INFINI_OK ? lay.total : 0;
+}
+
+int infini_attn_decode_step_q4(const void* q_t, const void* k_t, const void* v_t, const float* beta,
+                               const infini_cache_q4_t* cache, const int* pos, const float* M,
+                               const float* z, int seg_len, const infini_dims_t* dims, void* out_t,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+  Q4Layout lay;
+  CacheQ4 c;
+  int rc = q4_layout(dims, seg_len, &lay);
+  if (rc == INFINI_OK) rc = q4_shape(dims, seg_len, cache, &c);
+  if (rc != INFINI_OK) return rc;
+  if (!q_t || !k_t || !v_t || !beta || !pos || !M || !z || !out_t) return INFINI_ERR_ARG;
+  const void* ptrs[] = {q_t, k_t, v_t, beta, pos, M, z, out_t};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return INFINI_ERR_ALIGN;
+  if (workspace == nullptr && workspace_bytes != 0) return INFINI_ERR_ARG;
+  if (workspace && (workspace_bytes < lay.total || ((uintptr_t)workspace & (kAlign - 1)) != 0))
+    return INFINI_ERR_WORKSPACE;
+  const size_t elem = dims->dtype == INFINI_DTYPE_BF16 ? 2 : 4, d = dims->d_k;
+  const size_t BHq = (size_t)dims->B * dims->H_q, BHkv = (size_t)dims->B * dims->H_kv;
+  const Range ins[] = {rng(q_t, BHq * d * elem), rng(k_t, BHkv * d * elem), rng(v_t, BHkv * d * elem),
+                       rng(beta, (size_t)dims->H_q * 4), rng(pos, (size_t)dims->B * 4),
+                       rng(M, BHkv * d * d * 4), rng(z, BHkv * d * 4)};
+  const Range outs[] = {c.r[0], c.r[1], c.r[2], c.r[3], rng(out_t, BHq * d * elem),
+                        rng(workspace, workspace ? lay.total : 0)};
+  for (int i = 0; i < 6; ++i) {
+    for (const Range& r : ins)
+      if (overlap(outs[i], r)) return INFINI_ERR_ALIAS;
+    for (int j = i + 1; j < 6; ++j)
+      if (overlap(outs[i], outs[j])) return INFINI_ERR_ALIAS;
+  }
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  Q4Problem p = q4_problem(dims, seg_len, c);
+  p.status = status_ptr();
+  if (!p.status) return INFINI_ERR_CUDA;
+  char* ws = static_cast<char*>(workspace);
+  bool owned = false;
+  if (!ws) {
+    if (cudaMallocAsync(reinterpret_cast<void**>(&ws), lay.total, st) != cudaSuccess) return INFINI_ERR_CUDA;
+    owned = true;
+    if (cudaMemsetAsync(ws, 0, lay.part, st) != cudaSuccess) {
+      cudaFreeAsync(ws, st);
+      return INFINI_ERR_CUDA;
+    }
+  }
+  p.q_t = q_t; p.k_t = k_t; p.v_t = v_t; p.beta = beta; p.pos = pos; p.M = M; p.z = z; p.out_t = out_t;
+  p.ctr = reinterpret_cast<unsigned int*>(ws);
+  p.part = reinterpret_cast<float*>(ws + lay.part);
+  p.ret = reinterpret_cast<float*>(ws + lay.ret);
+  p.chunk = lay.chunk; p.nsplit = lay.nsplit;
+  cudaError_t e = launch_q4(p, Q4What::kStep, 1, nullptr, nullptr, st);
+  if (owned) {
+    cudaError_t f = cudaFreeAsync(ws, st);
+    if (e == cudaSuccess) e = f;
+  }
+  return e == cudaSuccess ? INFINI_OK : INFINI_ERR_CUDA;
+}
+
 int infini_attn_sync_status(void* stream) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (cudaStreamSynchronize(st) != cudaSuccess) return INFINI_ERR_CUDA;

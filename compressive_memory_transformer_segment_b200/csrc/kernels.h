@@ -200,6 +200,33 @@ struct W4PackProblem {
 enum class W4Layout { kQuantize, kPack, kDequantize };
 cudaError_t launch_w4_layout(const W4PackProblem& p, W4Layout what, cudaStream_t stream);
 
+// Segment buffer in 4 bits: the decode step over it, appending rows, reading
+// them back.  codes [B, H_kv, S, d / 2] bytes, scale [B, H_kv, S, d / 32, 2].
+struct Q4Problem {
+  const void* q_t;        // [B, H_q, d]
+  const void* k_t;        // [B, H_kv, d] (append: [B, H_kv, n, d])
+  const void* v_t;
+  const float* beta;      // [H_q]
+  uint8_t* k_codes;
+  __nv_bfloat16* k_scale;
+  uint8_t* v_codes;
+  __nv_bfloat16* v_scale;
+  const int* pos;         // [B]
+  const float* M;         // [B, H_kv, d, d]
+  const float* z;         // [B, H_kv, d]
+  void* out_t;            // [B, H_q, d]
+  float* part;            // workspace: [B * H_q][nsplit][d + 2]
+  float* ret;             // workspace: [B * H_q][d + 1]
+  unsigned int* ctr;      // workspace: [B * H_kv][head chunks] tickets, 0 between steps
+  int B, H_q, H_kv, d, S, chunk, nsplit;
+  bool bf16;
+  unsigned int* status;
+};
+enum class Q4What { kStep, kAppend, kRead };
+int q4_head_chunks(int g);
+int q4_chunk_rows(long long groups, int S);
+cudaError_t launch_q4(const Q4Problem& p, Q4What what, int n, void* k, void* v, cudaStream_t stream);
+
 int decode_splits(int S);
 int decode_head_chunks(int g);
 cudaError_t launch_decode_step(const DecodeProblem& p, cudaStream_t stream);

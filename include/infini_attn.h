@@ -485,6 +485,101 @@ INFINI_API int infini_attn_decode_step(const void* q_t, const void* k_t, const v
                                        const infini_dims_t* dims, void* out_t, void* workspace,
                                        size_t workspace_bytes, void* stream);
 
+/* A segment buffer in 4 bits: the rolling buffer of the streaming decode at
+ * 5 bits per value instead of 16 or 32.  Each row (one token of one KV head) is
+ * cut into groups of 32 channels; a channel's value is
+ *   scale q + minimum,  q in 0..15,
+ * with minimum = bf16(the group's least value), scale =
+ * bf16((greatest - minimum) / 15) and q = (value - minimum) / scale to the
+ * nearest, ties to even, cut to 0..15 (0 where scale is 0); fp32 arithmetic.  A group with a NaN,
+ * an infinity or a range beyond fp32 reads back as NaN.
+ *   k_codes, v_codes   device [B, H_kv, seg_len, d / 2] bytes
+ *   k_scale, v_scale   device bf16 [B, H_kv, seg_len, d / 32, 2]: scale,
+ *                      minimum
+ * Key codes: 32-bit word (d / 32) c + j of a row (c = 0..3, j = the group)
+ * holds channels 32 j + 8 c + o, o = 0..7, even o in bits 2 o .. 2 o + 3, odd
+ * o in bits 2 o + 14 .. 2 o + 17.  Value codes: 16-bit word (d / 32) i + j
+ * (i = 0..7) holds channels 32 j + 4 i + t, t = 0..3, in bits 4 t .. 4 t + 3.
+ * All little-endian.  The calls below take dims with B, H_kv, d_k = d_v = d in
+ * {32, 64, 128} and dtype (the element type of the rows given or returned),
+ * seg_len <= 2^30, B * H_q <= 65535, four arrays that do not overlap, 16-byte
+ * aligned.  Rows that a call does not write keep what they hold, and rows
+ * behind a stream's last one are never read. */
+typedef struct {
+  void* k_codes;
+  void* k_scale;
+  void* v_codes;
+  void* v_scale;
+} infini_cache_q4_t;
+
+/* Round rows into the buffer: k, v device [B, H_kv, L, d] (L = dims->L <=
+ * seg_len) go to rows pos[b] .. pos[b] + L - 1 of batch row b.
+ *   pos          device int32 [B]; -1 skips the batch row.  A row whose range
+ *                leaves the buffer is skipped and reported by
+ *                infini_attn_sync_status (INFINI_ERR_RANGE).
+ *   stream       cudaStream_t; asynchronous.
+ * dims->H_q is ignored.  Errors: INFINI_ERR_ARG, _UNSUPPORTED, _ALIGN, _ALIAS,
+ * _CUDA. */
+INFINI_API int infini_attn_cache_q4_append(const void* k, const void* v, const int* pos,
+                                           const infini_dims_t* dims, int seg_len,
+                                           const infini_cache_q4_t* cache, void* stream);
+
+/* The values of rows 0 .. L - 1 (L = dims->L <= seg_len), rounded to dtype:
+ * k, v device [B, H_kv, L, d].  dims->H_q is ignored.  Errors as above. */
+INFINI_API int infini_attn_cache_q4_read(const infini_cache_q4_t* cache, const infini_dims_t* dims,
+                                         int seg_len, void* k, void* v, void* stream);
+
+/* infini_attn_state_update with the first L = dims->L rows of a 4-bit buffer
+ * as one segment's keys and values (L = seg_len when the segment is full):
+ * (M_in, z_in) to (M_out, z_out), in place if equal.  dtype BF16 reads the
+ * values rounded to bf16 and takes the forward's tensor-core scan where it
+ * applies; F32 keeps them in fp32.  For streams that fill their segments at
+ * different times call it with B = 1 and pointers to that stream's part of each
+ * array.  dims->H_q is ignored.
+ *   workspace    infini_attn_state_update_q4_workspace_bytes bytes, 256-byte
+ *                aligned, or NULL with workspace_bytes == 0
+ * Errors: those of infini_attn_state_update. */
+INFINI_API size_t infini_attn_state_update_q4_workspace_bytes(const infini_dims_t* dims, int rule);
+INFINI_API int infini_attn_state_update_q4(const infini_cache_q4_t* cache, const float* M_in,
+                                           const float* z_in, int rule, const infini_dims_t* dims,
+                                           int seg_len, float* M_out, float* z_out,
+                                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of device workspace infini_attn_decode_step_q4 needs (0 if the sizes
+ * are invalid; dims->L is ignored).  Like infini_attn_decode_step's it must be
+ * zero-filled before its first step and serves one call at a time: calls that
+ * may run at the same time (two streams, two captured graphs) need one each. */
+INFINI_API size_t infini_attn_decode_q4_workspace_bytes(const infini_dims_t* dims, int seg_len);
+
+/* One decode step over a 4-bit segment buffer, every stream at its own
+ * position.  For each batch row b with 0 <= pos[b] < seg_len: k_t, v_t are
+ * rounded into row pos[b], and
+ *   out_t = sg(beta) A_mem + (1 - sg(beta)) A_dot
+ * as in infini_attn_decode_step, A_dot over the values of rows 0 .. pos[b] as
+ * the buffer holds them.  A batch row with pos[b] = -1 is idle: its part of the
+ * buffer and of out_t is left as it is.  Any other position is treated the
+ * same and reported by infini_attn_sync_status (INFINI_ERR_RANGE).
+ *   q_t, k_t, v_t, out_t, beta, M, z
+ *                as for infini_attn_decode_step; M and z are only read.  When a
+ *                segment is full (pos[b] = seg_len - 1) the caller updates
+ *                them with infini_attn_state_update_q4.
+ *   pos          device int32 [B], read by the kernel: a captured step serves
+ *                every position
+ *   dims         B, H_q (a multiple of H_kv), H_kv, d_k = d_v = d, dtype;
+ *                dims->L is ignored
+ *   workspace    infini_attn_decode_q4_workspace_bytes bytes, 256-byte aligned
+ *                (see there), or NULL with workspace_bytes == 0
+ *                (stream-ordered allocation, zeroed by the call)
+ *   stream       cudaStream_t; asynchronous.
+ * The buffer's arrays, out_t and the workspace overlap nothing.  Sums run in a
+ * fixed order: repeated calls are bitwise equal.  Errors: those of
+ * infini_attn_decode_step. */
+INFINI_API int infini_attn_decode_step_q4(const void* q_t, const void* k_t, const void* v_t,
+                                          const float* beta, const infini_cache_q4_t* cache,
+                                          const int* pos, const float* M, const float* z,
+                                          int seg_len, const infini_dims_t* dims, void* out_t,
+                                          void* workspace, size_t workspace_bytes, void* stream);
+
 /* Bytes of device arena infini_attn_forward_host needs: room for q, k, v,
  * beta, M, z, out and the workspace, each 256-byte aligned.  0 if invalid. */
 INFINI_API size_t infini_attn_host_arena_bytes(const infini_dims_t* dims, int seg_len, int rule);

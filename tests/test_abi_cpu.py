@@ -359,6 +359,82 @@ def test_w4_checks_arguments_on_the_host(lib):
     assert api.status_string(api.ERR_RANGE) != api.status_string(12345)
 
 
+def test_q4_checks_arguments_on_the_host(lib):
+    """Argument checks of the 4-bit segment buffer's calls return before any
+    CUDA call."""
+    MB = 1 << 20
+    d = api.make_dims(2, 4, 2, 3, 64, 64, 1)
+
+    def cache(**over):
+        c = dict(dict(k_codes=1 * MB, k_scale=2 * MB, v_codes=3 * MB, v_scale=4 * MB), **over)
+        return ctypes.byref(api._CacheQ4Ptrs(*c.values()))
+
+    n = lib.infini_attn_decode_q4_workspace_bytes(ctypes.byref(d), 100)
+    assert n >= 2 * 4 * (64 + 2) * 4
+    for bad in (api.make_dims(2, 3, 2, 1, 64, 64, 1), api.make_dims(0, 4, 2, 1, 64, 64, 1),
+                api.make_dims(2, 4, 2, 1, 64, 32, 1), api.make_dims(2, 4, 2, 1, 48, 48, 1),
+                api.make_dims(1 << 14, 4, 4, 1, 64, 64, 1)):
+        assert lib.infini_attn_decode_q4_workspace_bytes(ctypes.byref(bad), 100) == 0
+    assert lib.infini_attn_decode_q4_workspace_bytes(ctypes.byref(d), 0) == 0
+    assert lib.infini_attn_decode_q4_workspace_bytes(ctypes.byref(d), (1 << 30) + 1) == 0
+    good = dict(q=5 * MB, k=6 * MB, v=7 * MB, beta=8 * MB, cache=cache(), pos=9 * MB, M=10 * MB, z=11 * MB,
+                seg=100, dims=ctypes.byref(d), out=12 * MB, ws=16 * MB, ws_n=n)
+
+    def step(**over):
+        return lib.infini_attn_decode_step_q4(*dict(good, **over).values(), None)
+
+    for name in ("q", "k", "v", "beta", "cache", "pos", "M", "z", "out", "dims"):
+        assert step(**{name: None}) == api.ERR_ARG, name
+    for name in ("k_codes", "k_scale", "v_codes", "v_scale"):
+        assert step(cache=cache(**{name: None})) == api.ERR_ARG
+        assert step(cache=cache(**{name: 32 * MB + 8})) == api.ERR_ALIGN
+        assert step(cache=cache(**{name: 12 * MB + 64})) == api.ERR_ALIAS     # over the output
+        assert step(cache=cache(**{name: good["M"] + 64})) == api.ERR_ALIAS   # over an input
+    assert step(cache=cache(v_codes=1 * MB + 512)) == api.ERR_ALIAS           # over each other
+    assert step(seg=0) == api.ERR_ARG
+    assert step(out=good["q"]) == api.ERR_ALIAS
+    assert step(pos=9 * MB + 4) == api.ERR_ALIGN
+    assert step(ws_n=n - 1) == api.ERR_WORKSPACE
+    assert step(ws=16 * MB + 64) == api.ERR_WORKSPACE
+    assert step(ws=None) == api.ERR_ARG
+    assert step(ws=good["z"]) == api.ERR_ALIAS
+    assert step(dims=ctypes.byref(api.make_dims(2, 4, 2, 1, 64, 64, 5))) == api.ERR_ARG
+
+    def append(k=5 * MB, v=6 * MB, pos=7 * MB, dims=d, seg=100, c=None):
+        return lib.infini_attn_cache_q4_append(k, v, pos, ctypes.byref(dims), seg, c or cache(), None)
+
+    assert append(k=None) == api.ERR_ARG
+    assert append(pos=None) == api.ERR_ARG
+    assert append(seg=2) == api.ERR_ARG                                       # 3 rows into 2
+    assert append(dims=api.make_dims(2, 4, 2, 0, 64, 64, 1)) == api.ERR_ARG
+    assert append(k=3 * MB) == api.ERR_ALIAS
+    assert append(v=6 * MB + 4) == api.ERR_ALIGN
+
+    def read(k=5 * MB, v=6 * MB, dims=d, seg=100):
+        return lib.infini_attn_cache_q4_read(cache(), ctypes.byref(dims), seg, k, v, None)
+
+    assert read(k=None) == api.ERR_ARG
+    assert read(seg=2) == api.ERR_ARG
+    assert read(k=6 * MB) == api.ERR_ALIAS
+    assert read(v=4 * MB) == api.ERR_ALIAS
+
+    need = lib.infini_attn_state_update_q4_workspace_bytes(ctypes.byref(d), 0)
+    assert need > 2 * 2 * 2 * 3 * 64 * 4
+    assert lib.infini_attn_state_update_q4_workspace_bytes(ctypes.byref(d), 9) == 0
+
+    def update(M=5 * MB, z=6 * MB, rule=0, dims=d, seg=100, Mo=7 * MB, zo=8 * MB, ws=16 * MB, ws_n=need):
+        return lib.infini_attn_state_update_q4(cache(), M, z, rule, ctypes.byref(dims), seg, Mo, zo, ws, ws_n,
+                                               None)
+
+    assert update(M=None) == api.ERR_ARG
+    assert update(rule=5) == api.ERR_ARG
+    assert update(seg=2) == api.ERR_ARG
+    assert update(ws_n=need - 1) == api.ERR_WORKSPACE
+    assert update(Mo=8 * MB - 64) == api.ERR_ALIAS
+    assert update(zo=5 * MB) == api.ERR_ALIAS
+    assert update(ws=1 * MB) == api.ERR_ALIAS
+
+
 def test_plain_c_program_uses_the_boundary(tmp_path):
     """The header compiles as C99 and a C program linked against the library
     gets the documented answers from the host-side calls (no GPU needed)."""
