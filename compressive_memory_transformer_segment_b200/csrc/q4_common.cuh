@@ -30,11 +30,6 @@ __device__ __forceinline__ void unpack_codes(uint32_t w, uint32_t bias, uint32_t
   }
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
 // bf16x2 of (lo, hi), and what it leaves of them: lo and hi become the
 // rounding errors.  Three such steps hold all 24 bits of an fp32.
 __device__ __forceinline__ uint32_t split_bf16(float& lo, float& hi) {
@@ -55,6 +50,13 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
       "{%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 2^x by the hardware approximation (relative error 2^-22; 0 below 2^-126).
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // Loads of data that passes through once (kept out of L1).

@@ -30,6 +30,8 @@
 // last one of them to finish (a ticket) merges and writes the output.  The
 // number of rows is read from device memory, so one captured launch serves
 // every position.
+#include <cuda_fp16.h>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "q4_common.cuh"
@@ -38,7 +40,16 @@ namespace infini {
 
 namespace {
 
-constexpr int kThreads = 256;
+#ifndef QT
+#define QT 256
+#endif
+#ifndef QB
+#define QB 2
+#endif
+#ifndef QW
+#define QW 4
+#endif
+constexpr int kThreads = QT;
 constexpr int kWarps = kThreads / 32;
 constexpr int kHeads = 8;               // query heads of a CTA (columns of a product)
 constexpr int kUnit = kWarps * 16;      // rows a CTA takes at a time
@@ -50,27 +61,17 @@ template <> struct RawBytes<4> { using type = uint32_t; };
 template <> struct RawBytes<8> { using type = uint2; };
 template <> struct RawBytes<16> { using type = uint4; };
 
-__device__ __forceinline__ void ld_once(const void* p, uint4& r) { r = ld_once_16(p); }
-__device__ __forceinline__ void ld_once(const void* p, uint2& r) {
-  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
-}
-__device__ __forceinline__ void ld_once(const void* p, uint32_t& r) {
-  asm volatile("ld.global.L1::no_allocate.u32 %0, [%1];" : "=r"(r) : "l"(p));
-}
-__device__ __forceinline__ void ld_once(const void* p, unsigned short& r) {
-  asm volatile("ld.global.L1::no_allocate.u16 %0, [%1];" : "=h"(r) : "l"(p));
-}
-
 template <int BYTES>
 struct Raw {
   typename RawBytes<BYTES>::type v;
-  __device__ __forceinline__ void load(const void* p, bool in) {
-    v = {};
-    if (in) ld_once(p, v);
+  __device__ __forceinline__ void load(const uint8_t* p) { v = *reinterpret_cast<const decltype(v)*>(p); }
+  __device__ __forceinline__ uint32_t word(int j) const {
+    if constexpr (BYTES == 2) return v;
+    else return reinterpret_cast<const uint32_t*>(&v)[j];
   }
-  __device__ __forceinline__ uint32_t word(int j) const { return reinterpret_cast<const uint32_t*>(&v)[j]; }
-  __device__ __forceinline__ uint32_t half(int j) const {
-    return reinterpret_cast<const unsigned short*>(&v)[j];
+  // Halfword j of this and of `other`, in the low and the high half.
+  __device__ __forceinline__ uint32_t half_pair(const Raw& other, int j) const {
+    return __byte_perm(word(j / 2), other.word(j / 2), j % 2 == 0 ? 0x5410 : 0x7632);
   }
   // Scale and minimum of group j (a bf16 pair).
   __device__ __forceinline__ float scale(int j) const { return __uint_as_float(word(j) << 16); }
@@ -97,82 +98,425 @@ __device__ __forceinline__ float column_max(float x) {
   return x;
 }
 
-// One row x[0..D-1] into the buffer, by one warp: lane l holds channel l of
-// each group.  fp32 arithmetic with one rounding per operation; a group with
-// a NaN becomes NaN.
-template <typename T, int D, bool KEY>
-__device__ __forceinline__ void store_row(const T* x, uint8_t* codes, __nv_bfloat16* sm, int lane) {
+// 8 channels 8 w .. 8 w + 7 of a row, held by one lane, into the buffer; the 4
+// lanes of a 32-channel group are neighbours and call together.  fp32
+// arithmetic with one rounding per operation; a group with a NaN becomes NaN.
+template <int D, bool KEY>
+__device__ __forceinline__ void store_group(const float (&x)[8], int w, uint8_t* codes, __nv_bfloat16* sm,
+                                            bool active) {
   constexpr int NJ = D / 32;
-  float v[NJ];
+  const int j = w >> 2, c = w & 3;
+  float lo = x[0], hi = x[0];
+  int nan = x[0] != x[0];
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) v[j] = to_f32<T>(x[32 * j + lane]);
-#pragma unroll
-  for (int j = 0; j < NJ; ++j) {
-    const float lo = -warp_max(-v[j]), hi = warp_max(v[j]);
-    __nv_bfloat162 par;
-    par.y = __float2bfloat16_rn(lo);
-    const float m = __bfloat162float(par.y);
-    par.x = __float2bfloat16_rn(__fmul_rn(fmaxf(__fsub_rn(hi, m), 0.f), 1.f / 15.f));
-    const float s = __bfloat162float(par.x);
-    if (__any_sync(0xffffffffu, v[j] != v[j])) par = __floats2bfloat162_rn(NAN, NAN);
-    const float t = s > 0.f ? rintf(__fdiv_rn(__fsub_rn(v[j], m), s)) : 0.f;
-    const uint32_t q = (uint32_t)fminf(fmaxf(t, 0.f), 15.f);
-    if constexpr (KEY) {
-      const int o = lane & 7, c = lane >> 3;
-      uint32_t w = q << ((o & 1) ? 2 * o + 14 : 2 * o);
-      w |= __shfl_xor_sync(0xffffffffu, w, 1);
-      w |= __shfl_xor_sync(0xffffffffu, w, 2);
-      w |= __shfl_xor_sync(0xffffffffu, w, 4);
-      if (o == 0) reinterpret_cast<uint32_t*>(codes)[c * NJ + j] = w;
-    } else {
-      const int t4 = lane & 3, i = lane >> 2;
-      uint32_t w = q << (4 * t4);
-      w |= __shfl_xor_sync(0xffffffffu, w, 1);
-      w |= __shfl_xor_sync(0xffffffffu, w, 2);
-      if (t4 == 0) reinterpret_cast<unsigned short*>(codes)[i * NJ + j] = (unsigned short)w;
-    }
-    if (lane == 0) reinterpret_cast<__nv_bfloat162*>(sm)[j] = par;
+  for (int e = 1; e < 8; ++e) {
+    lo = fminf(lo, x[e]);
+    hi = fmaxf(hi, x[e]);
+    nan |= x[e] != x[e];
   }
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) {
+    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    nan |= __shfl_xor_sync(0xffffffffu, nan, o);
+  }
+  __nv_bfloat162 par;
+  par.y = __float2bfloat16_rn(lo);
+  const float m = __bfloat162float(par.y);
+  par.x = __float2bfloat16_rn(__fmul_rn(fmaxf(__fsub_rn(hi, m), 0.f), 1.f / 15.f));
+  const float s = __bfloat162float(par.x);
+  if (nan) par = __floats2bfloat162_rn(NAN, NAN);
+  uint32_t q[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float t = s > 0.f ? rintf(__fdiv_rn(__fsub_rn(x[e], m), s)) : 0.f;
+    q[e] = (uint32_t)fminf(fmaxf(t, 0.f), 15.f);
+  }
+  if (!active) return;
+  if constexpr (KEY) {
+    uint32_t word = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) word |= q[e] << ((e & 1) ? 2 * e + 14 : 2 * e);
+    reinterpret_cast<uint32_t*>(codes)[c * NJ + j] = word;
+  } else {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      uint32_t half = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) half |= q[4 * u + e] << (4 * e);
+      reinterpret_cast<unsigned short*>(codes)[(2 * c + u) * NJ + j] = (unsigned short)half;
+    }
+  }
+  if (c == 0) reinterpret_cast<__nv_bfloat162*>(sm)[j] = par;
 }
 
-// The queries of head i at 8 channels as B fragments of `parts` bf16 parts.
+// 8 consecutive elements as floats (16- or 32-byte aligned).
+__device__ __forceinline__ void load8(const __nv_bfloat16* x, float (&v)[8]) {
+  const uint4 r = *reinterpret_cast<const uint4*>(x);
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    v[2 * e] = __uint_as_float(w[e] << 16);
+    v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void load8(const float* x, float (&v)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(x)[0], b = reinterpret_cast<const float4*>(x)[1];
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* x, const float (&v)[8]) {
+  uint4 r;
+  uint32_t* w = reinterpret_cast<uint32_t*>(&r);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+    w[e] = *reinterpret_cast<const uint32_t*>(&t);
+  }
+  *reinterpret_cast<uint4*>(x) = r;
+}
+__device__ __forceinline__ void store8(float* x, const float (&v)[8]) {
+  reinterpret_cast<float4*>(x)[0] = {v[0], v[1], v[2], v[3]};
+  reinterpret_cast<float4*>(x)[1] = {v[4], v[5], v[6], v[7]};
+}
+
+// One row x[0..D-1] into the buffer, by one warp (D / 8 of its lanes).
+template <typename T, int D, bool KEY>
+__device__ __forceinline__ void store_row(const T* x, uint8_t* codes, __nv_bfloat16* sm, int lane) {
+  const bool active = lane < D / 8;
+  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (active) load8(x + 8 * lane, v);
+  store_group<D, KEY>(v, lane & (D / 8 - 1), codes, sm, active);
+}
+
+// fp16 parts that hold a query or a probability of this type.
 template <typename T> struct Parts;
 template <> struct Parts<__nv_bfloat16> { static constexpr int n = 1; };
-template <> struct Parts<float> { static constexpr int n = 3; };
+template <> struct Parts<float> { static constexpr int n = 2; };
 
-// One warp's 16 rows as loaded: keys of rows i, i + 8 (chunk c), values of
-// rows 2c, 2c + 1, 2c + 8, 2c + 9 (chunk i), and the parameters of rows i,
-// i + 8.  Rows from r1 on read as zero, whatever the buffer holds there.
+// One warp's 16 rows, as a lane needs them: keys of rows k_row(i), + 8 (chunk
+// c), values of rows c, 4 + (c ^ 1), + 8, + 8 (chunk i), and the parameters of
+// rows k_row(i), + 8.  The product's index along the rows (i, or 2c and 2c + 1)
+// stands for row k_row(index) of its eight: an order in which the key loads
+// have no bank conflict and the value loads two-way ones.
+__device__ __forceinline__ int k_row(int i) { return (i & 1) ? 4 + ((i >> 1) ^ 1) : i >> 1; }
+
 template <int D>
 struct Tile {
   Raw<D / 8> k[2];
   Raw<D / 8> kp[2], vp[2];
   Raw<D / 16> v[4];
-  __device__ __forceinline__ void load(const Q4Problem& p, size_t bh, int r, int r1, int i, int c) {
-    const size_t row0 = bh * p.S;
+};
+
+// A warp's ring of tiles in shared memory, filled by asynchronous copies: the
+// loads of the next kStages - 1 tiles are in flight while one is used, without
+// registers to hold them.
+template <int D>
+struct Ring {
+  static constexpr int kCodes = 16 * (D / 2), kParams = 16 * (D / 8);  // bytes of 16 rows
+  static constexpr int kSlot = 2 * kCodes + 2 * kParams;
+  #ifndef QS
+#define QS 4
+#endif
+  static constexpr int kStages = QS;
+  uint8_t* smem;
+  const uint8_t *k, *v, *par;  // this lane's source in the chunk's first 16 rows
+  int n, lane;                 // rows of the chunk
+
+  __device__ __forceinline__ Ring(const Q4Problem& p, uint8_t* ring, size_t row0, int rows, int lane_)
+      : smem(ring), n(rows), lane(lane_) {
+    const int chunk = D == 32 ? lane & 15 : lane;  // 16-byte pieces: D / 32 per row
+    k = p.k_codes + row0 * (D / 2) + chunk * 16;
+    v = p.v_codes + row0 * (D / 2) + chunk * 16;
+    par = reinterpret_cast<const uint8_t*>(lane < 16 ? p.k_scale : p.v_scale) + (row0 + (lane & 15)) * (D / 8);
+  }
+  template <int BYTES>
+  __device__ __forceinline__ static void copy(uint8_t* dst, const uint8_t* src, bool in) {
+    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+    const int size = in ? BYTES : 0;  // the rest is filled with zeros
+    if constexpr (BYTES == 16)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src), "r"(size) : "memory");
+    else
+      asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to), "l"(src), "n"(BYTES), "r"(size)
+                   : "memory");
+  }
+  // Starts the copy of rows r .. r + 15; rows from n on become zeros, whatever
+  // the buffer holds there (their addresses are not read).
+  __device__ __forceinline__ void fill(int slot, int r) const {
+    uint8_t* s = smem + slot * kSlot;
+    const size_t off = (size_t)r * (D / 2);
+    if constexpr (D == 32) {
+      const bool in = r + (lane & 15) < n;
+      copy<16>(s + lane * 16, (lane < 16 ? k : v) + (in ? off : 0), in);
+    } else {
+      constexpr int PR = D / 32;  // pieces per row
+#pragma unroll
+      for (int e = 0; e < kCodes / 512; ++e) {
+        const bool in = r + (lane + 32 * e) / PR < n;
+        copy<16>(s + (lane + 32 * e) * 16, k + (in ? off + 512 * e : 0), in);
+        copy<16>(s + kCodes + (lane + 32 * e) * 16, v + (in ? off + 512 * e : 0), in);
+      }
+    }
+    const bool in = r + (lane & 15) < n;
+    copy<D / 8>(s + 2 * kCodes + lane * (D / 8), par + (in ? (size_t)r * (D / 8) : 0), in);
+  }
+  __device__ __forceinline__ static void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  // Waits until at most kStages - 1 groups of this lane are in flight.
+  __device__ __forceinline__ static void wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+  }
+  __device__ __forceinline__ void read(Tile<D>& t, int slot) const {
+    const uint8_t* s = smem + slot * kSlot;
+    const int i = lane >> 2, c = lane & 3, kr = k_row(i);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int row = r + i + 8 * e;
-      const bool in = row < r1;
-      k[e].load(p.k_codes + (row0 + row) * (D / 2) + c * (D / 8), in);
-      kp[e].load(p.k_scale + (row0 + row) * (D / 16), in);
-      vp[e].load(p.v_scale + (row0 + row) * (D / 16), in);
+      t.k[e].load(s + (kr + 8 * e) * (D / 2) + c * (D / 8));
+      t.kp[e].load(s + 2 * kCodes + (kr + 8 * e) * (D / 8));
+      t.vp[e].load(s + 2 * kCodes + kParams + (kr + 8 * e) * (D / 8));
+      t.v[2 * e].load(s + kCodes + (c + 8 * e) * (D / 2) + i * (D / 16));
+      t.v[2 * e + 1].load(s + kCodes + (4 + (c ^ 1) + 8 * e) * (D / 2) + i * (D / 16));
     }
+  }
+};
+
+// 4-bit codes as fp16 operands without arithmetic: the fp16 with the bits of a
+// small integer n is n 2^-24 (subnormals, and the first exponent, are linear
+// up to 2^11 2^-24), so masking is all the conversion there is.  Of the four
+// codes of a 16-bit half the first and third (after one shift by 8) come out as
+// q, the second and fourth, masked where they stand, as 16 q; whoever uses
+// them has 1/16 in the other operand or in the result.
+__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t (&out)[4]) {
+  out[0] = w & 0x000f000fu;
+  out[1] = w & 0x00f000f0u;
+  out[2] = (w >> 8) & 0x000f000fu;
+  out[3] = (w >> 8) & 0x00f000f0u;
+}
+// The tensor cores align such products by their operands' exponents, zeros in
+// front included, which leaves about 2^-16 of a sum: right for bf16 heads, not
+// for fp32 ones.  Those take q - 8 as a normal number: 1024 + q by insertion,
+// minus 1032; 1024 + 16 q, over 16 and minus 72 (both exact).
+template <bool EXACT>
+__device__ __forceinline__ void code_pairs(uint32_t w, uint32_t (&out)[4]) {
+  codes_f16(w, out);
+  if constexpr (EXACT) {
+    const __half2 one = __floats2half2_rn(-1032.f, -1032.f), sixteenth = __floats2half2_rn(0.0625f, 0.0625f),
+                  shift = __floats2half2_rn(-72.f, -72.f);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int row = r + 2 * c + (e & 1) + 8 * (e >> 1);
-      v[e].load(p.v_codes + (row0 + row) * (D / 2) + i * (D / 16), row < r1);
+      const uint32_t bits = out[e] | 0x64006400u;
+      const __half2 n = *reinterpret_cast<const __half2*>(&bits);
+      const __half2 v = e % 2 == 0 ? __hadd2(n, one) : __hfma2(n, sixteenth, shift);
+      out[e] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+  }
+}
+
+// f16x2 of (lo, hi), and what it leaves of them.
+__device__ __forceinline__ uint32_t split_f16(float& lo, float& hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  lo -= __low2float(v);
+  hi -= __high2float(v);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                              uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// 2^e, -126 <= e <= 127.
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
+
+// Running attention of one warp over its rows, for 8 heads: fragments of
+// heads 2c, 2c + 1.  The operands that meet the codes are fp16 (bf16 heads:
+// one part, 2^-12 of a term; fp32 heads: two, 2^-23), kept in its range by
+// powers of two: a head's query by its largest element, the probabilities
+// times scale by the largest scale seen.
+template <int D, int NP>
+struct Attention {
+  static constexpr int NJ = D / 32;
+  static constexpr bool kExact = NP > 1;
+  static constexpr float kUnit1 = kExact ? 1.f : 0x1p24f;        // of a product with q, or with q - 8
+  static constexpr float kOdd = kExact ? 1.f : 0.0625f;          // second and fourth codes
+  static constexpr float kCenter = kExact ? 8.f : 0.f;
+  uint32_t qf[NJ][NP][4];  // queries of head i as B fragments, times 2^e (pairs 1, 3: kOdd of that)
+  float qsum[NJ][2];       // sum of a head's scaled query over each group, in units of a code
+  float f1, f2[2];         // log2(e) / sqrt(d) kUnit1, 2^-e: scores to powers of two
+  float m[2], l[2];        // running maximum; sum over this lane's rows
+  float o[2 * NJ][4];      // O^T without the minima, times 2^-pe / kUnit1 (rows i + 8: over kOdd too)
+  float omin[NJ][2];       // sum of p (minimum + kCenter scale) over this lane's rows
+  int pe;                  // p scale 2^-pe is what the products get
+  uint32_t limit;          // bf16 bits of the largest scale that 2^-pe holds below 2^15
+
+  // q_t: this KV head's first query; ng: heads of it that exist.
+  template <typename T>
+  __device__ __forceinline__ void init(const T* q_t, int ng, int lane) {
+    const int i = lane >> 2, c = lane & 3;
+    float x[NJ][8], top = 0.f;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[j][e] = 0.f;
+      if (i < ng) load8(q_t + (size_t)i * D + 32 * j + 8 * c, x[j]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[j][e]));
+    }
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    // The largest element goes to 2^14 .. 2^15.
+    const int e = min(14 + 127 - (__float_as_int(top) >> 23), 100);
+    const float up = pow2(e);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      float s = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        x[j][k] *= up;
+        s += x[j][k];
+      }
+      s += __shfl_xor_sync(0xffffffffu, s, 1);
+      s += __shfl_xor_sync(0xffffffffu, s, 2);
+      qsum[j][0] = __shfl_sync(0xffffffffu, s, 8 * c) * (1.f / kUnit1);
+      qsum[j][1] = __shfl_sync(0xffffffffu, s, 8 * c + 4) * (1.f / kUnit1);
+#pragma unroll
+      for (int k = 2; k < 8; k += 4) {
+        x[j][k] *= kOdd;
+        x[j][k + 1] *= kOdd;
+      }
+#pragma unroll
+      for (int part = 0; part < NP; ++part)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) qf[j][part][k] = split_f16(x[j][2 * k], x[j][2 * k + 1]);
+      omin[j][0] = omin[j][1] = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[2 * j][k] = o[2 * j + 1][k] = 0.f;
+    }
+    f1 = rsqrtf((float)D) * 1.4426950408889634f * kUnit1;
+    f2[0] = pow2(-__shfl_sync(0xffffffffu, e, 8 * c));
+    f2[1] = pow2(-__shfl_sync(0xffffffffu, e, 8 * c + 4));
+    m[0] = m[1] = -INFINITY;
+    l[0] = l[1] = 0.f;
+    pe = -120;
+    limit = 0;
+  }
+
+  // A scale beyond the limit: the unit moves so that the largest of these rows
+  // lies at 2^7 .. 2^8 (the first rows set it so).
+  __device__ __forceinline__ void raise(uint32_t top) {
+    top = __reduce_max_sync(0xffffffffu, top);
+    const int to = max(min((int)(top >> 7), 255) - 127 - 7, -120);
+    const float down = exp2f((float)(pe - to));
+#pragma unroll
+    for (int j = 0; j < 2 * NJ; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[j][e] *= down;
+    pe = to;
+    limit = min(to + 15 + 127, 255) << 7;
+  }
+
+  __device__ __forceinline__ void step(const Tile<D>& t, bool in0, bool in1) {
+    // Scores of rows i (s[0], s[1]) and i + 8 (s[2], s[3]).
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      uint32_t fa[4], fb[4];
+      code_pairs<kExact>(t.k[0].word(j), fa);
+      code_pairs<kExact>(t.k[1].word(j), fb);
+      float d[4];
+      mma_f16_first(d, fa[0], fb[0], fa[1], fb[1], qf[j][0][0], qf[j][0][1]);
+      mma_f16(d, fa[2], fb[2], fa[3], fb[3], qf[j][0][2], qf[j][0][3]);
+#pragma unroll
+      for (int part = 1; part < NP; ++part) {
+        mma_f16(d, fa[0], fb[0], fa[1], fb[1], qf[j][part][0], qf[j][part][1]);
+        mma_f16(d, fa[2], fb[2], fa[3], fb[3], qf[j][part][2], qf[j][part][3]);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float sc = t.kp[e].scale(j);
+        const float mn = kExact ? fmaf(kCenter, sc, t.kp[e].minimum(j)) : t.kp[e].minimum(j);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) s[2 * e + h] = fmaf(sc, d[2 * e + h], fmaf(mn, qsum[j][h], s[2 * e + h]));
+      }
+    }
+    float pr[4], corr[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float s0 = in0 ? s[h] * f1 * f2[h] : -INFINITY, s1 = in1 ? s[2 + h] * f1 * f2[h] : -INFINITY;
+      const float mn = fmaxf(m[h], column_max(fmaxf(s0, s1)));
+      corr[h] = exp2_approx(m[h] - mn);  // 0 for the first rows
+      m[h] = mn;
+      pr[h] = exp2_approx(s0 - mn);
+      pr[2 + h] = exp2_approx(s1 - mn);
+      l[h] = fmaf(l[h], corr[h], pr[h] + pr[2 + h]);
+    }
+    // The maximum rarely moves after the first rows (written so that a NaN
+    // rescales too).
+    if (__any_sync(0xffffffffu, !(corr[0] == 1.f && corr[1] == 1.f))) {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          omin[j][h] *= corr[h];
+          o[2 * j][h] *= corr[h]; o[2 * j][2 + h] *= corr[h];
+          o[2 * j + 1][h] *= corr[h]; o[2 * j + 1][2 + h] *= corr[h];
+        }
+    }
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) top = __vimax3_u16x2(top, t.vp[0].word(j), t.vp[1].word(j));
+    top &= 0xffffu;  // the scales are the low halves
+    if (__any_sync(0xffffffffu, top > limit)) raise(top);
+    const float p2 = pow2(-pe);
+    float w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = pr[e] * p2;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      // Codes of group j: element t of a lane's four is channel 32 j + 4 i + t,
+      // indexes 2c, 2c + 1 (lo) and 2c + 8, 2c + 9 (hi) along the rows.
+      uint32_t lo[4], hi[4];
+      code_pairs<kExact>(t.v[0].half_pair(t.v[1], j), lo);
+      code_pairs<kExact>(t.v[2].half_pair(t.v[3], j), hi);
+      float ws[4];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float sc = t.vp[e].scale(j);
+        const float mn = kExact ? fmaf(kCenter, sc, t.vp[e].minimum(j)) : t.vp[e].minimum(j);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          ws[2 * e + h] = w[2 * e + h] * sc;
+          omin[j][h] = fmaf(pr[2 * e + h], mn, omin[j][h]);
+        }
+      }
+#pragma unroll
+      for (int part = 0; part < NP; ++part) {
+        const uint32_t b0 = transpose8(split_f16(ws[0], ws[1])), b1 = transpose8(split_f16(ws[2], ws[3]));
+        mma_f16(o[2 * j], lo[0], lo[1], hi[0], hi[1], b0, b1);
+        mma_f16(o[2 * j + 1], lo[2], lo[3], hi[2], hi[3], b0, b1);
+      }
     }
   }
 };
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, Parts<T>::n == 1 ? 2 : 1)
+__global__ void __launch_bounds__(kThreads, Parts<T>::n == 1 ? QB : 1)
 q4_decode_kernel(Q4Problem p) {
   constexpr int NJ = D / 32;           // groups
   constexpr int E = D / 32;            // channels per lane in the merges
   constexpr int NP = Parts<T>::n;
-  __shared__ float red[kWarps][kHeads][D + 2];
+  extern __shared__ __align__(16) uint8_t smem[];
+  float(*red)[kHeads][D + 2] = reinterpret_cast<float(*)[kHeads][D + 2]>(smem);  // [kWarps]
   __shared__ int last;
 
   const int bh = blockIdx.y;
@@ -207,122 +551,52 @@ q4_decode_kernel(Q4Problem p) {
                                p.v_scale + row * (D / 16), lane);
       __syncthreads();
     }
-    int r = r0 + warp * 16;
-    Tile<D> next;
-    if (r < r1) next.load(p, bh, r, r1, i, c);
-
-    // Queries of head i as B fragments, and every head's sum over each group.
-    uint32_t qf[NJ][NP][4];
-    float qsum[NJ][2];
+    const Ring<D> ring(p, smem + warp * Ring<D>::kStages * Ring<D>::kSlot, (size_t)bh * p.S + r0, r1 - r0, lane);
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      float x[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = 0.f;
-      if (i < ng) {
-        const T* src = q_t + (size_t)i * D + 32 * j + 8 * c;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = to_f32<T>(src[e]);
-      }
-      float s = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) s += x[e];
-      s += __shfl_xor_sync(0xffffffffu, s, 1);
-      s += __shfl_xor_sync(0xffffffffu, s, 2);
-      qsum[j][0] = __shfl_sync(0xffffffffu, s, 8 * c);
-      qsum[j][1] = __shfl_sync(0xffffffffu, s, 8 * c + 4);
-#pragma unroll
-      for (int part = 0; part < NP; ++part)
-#pragma unroll
-        for (int t = 0; t < 4; ++t) qf[j][part][t] = split_bf16(x[2 * t], x[2 * t + 1]);
+    for (int e = 0; e < Ring<D>::kStages; ++e) {
+      const int r = warp * 16 + e * kUnit;
+      if (r < ring.n) ring.fill(e, r);
+      ring.commit();
     }
-    const float sl2 = rsqrtf((float)D) * 1.4426950408889634f;
-
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // heads 2c, 2c + 1; l over rows i, i + 8
-    float o[2 * NJ][4], omin[NJ][2];
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      omin[j][0] = omin[j][1] = 0.f;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[2 * j][e] = o[2 * j + 1][e] = 0.f;
+    Attention<D, NP> at;
+    at.init(q_t, ng, lane);
+    const int kr = k_row(i);
+    int slot = 0;
+    for (int r = warp * 16; r < ring.n; r += kUnit) {
+      ring.wait();
+      __syncwarp();
+      Tile<D> t;
+      ring.read(t, slot);
+      __syncwarp();  // every lane has read the slot
+      const int ahead = r + Ring<D>::kStages * kUnit;
+      if (ahead < ring.n) ring.fill(slot, ahead);
+      ring.commit();
+      at.step(t, r + kr < ring.n, r + kr + 8 < ring.n);
+      slot = slot + 1 < Ring<D>::kStages ? slot + 1 : 0;
     }
-    for (; r < r1; r += kUnit) {
-      const Tile<D> cur = next;
-      if (r + kUnit < r1) next.load(p, bh, r + kUnit, r1, i, c);
-      // Scores of rows i (s[0], s[1]) and i + 8 (s[2], s[3]).
-      float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        uint32_t fa[4], fb[4];
-        unpack_codes(cur.k[0].word(j), kCodeBias2, fa);
-        unpack_codes(cur.k[1].word(j), kCodeBias2, fb);
-        float t[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int part = 0; part < NP; ++part) {
-          mma_bf16(t, fa[0], fb[0], fa[1], fb[1], qf[j][part][0], qf[j][part][1]);
-          mma_bf16(t, fa[2], fb[2], fa[3], fb[3], qf[j][part][2], qf[j][part][3]);
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          s[e] = fmaf(cur.kp[e >> 1].scale(j), t[e], fmaf(cur.kp[e >> 1].minimum(j), qsum[j][e & 1], s[e]));
-      }
-      const bool in0 = r + i < r1, in1 = r + i + 8 < r1;
-      float pr[4];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float s0 = in0 ? s[h] * sl2 : -INFINITY, s1 = in1 ? s[2 + h] * sl2 : -INFINITY;
-        const float mn = fmaxf(m[h], column_max(fmaxf(s0, s1)));
-        const float corr = exp2f(m[h] - mn);  // 0 for the first rows
-        m[h] = mn;
-        pr[h] = exp2f(s0 - mn);
-        pr[2 + h] = exp2f(s1 - mn);
-        l[h] = fmaf(l[h], corr, pr[h] + pr[2 + h]);
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-          omin[j][h] = fmaf(pr[h], cur.vp[0].minimum(j), fmaf(pr[2 + h], cur.vp[1].minimum(j), omin[j][h] * corr));
-          o[2 * j][h] *= corr; o[2 * j][2 + h] *= corr;
-          o[2 * j + 1][h] *= corr; o[2 * j + 1][2 + h] *= corr;
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        // Codes of group j: element t of a lane's four is channel
-        // 32 j + 4 i + t, rows 2c, 2c + 1 (lo) and 2c + 8, 2c + 9 (hi).
-        uint32_t lo[4], hi[4];
-        unpack_codes(cur.v[0].half(j) | (cur.v[1].half(j) << 16), kCodeBias2, lo);
-        unpack_codes(cur.v[2].half(j) | (cur.v[3].half(j) << 16), kCodeBias2, hi);
-        float w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = pr[e] * cur.vp[e >> 1].scale(j);
-#pragma unroll
-        for (int part = 0; part < NP; ++part) {
-          const uint32_t b0 = transpose8(split_bf16(w[0], w[1])), b1 = transpose8(split_bf16(w[2], w[3]));
-          mma_bf16(o[2 * j], lo[0], lo[1], hi[0], hi[1], b0, b1);
-          mma_bf16(o[2 * j + 1], lo[2], lo[3], hi[2], hi[3], b0, b1);
-        }
-      }
-    }
+    __syncthreads();  // the sums below lie where the rings were
     // This warp's (max, sum, acc) of heads 2c, 2c + 1.
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      l[h] = column_sum(l[h]);
+      at.l[h] = column_sum(at.l[h]);
       if (i == 0) {
-        red[warp][2 * c + h][D] = m[h];
-        red[warp][2 * c + h][D + 1] = l[h];
+        red[warp][2 * c + h][D] = at.m[h];
+        red[warp][2 * c + h][D + 1] = at.l[h];
       }
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
-        const float add = column_sum(omin[j][h]);
+        const float add = column_sum(at.omin[j][h]), unit = exp2f((float)at.pe);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          red[warp][2 * c + h][32 * j + 4 * i + 2 * u] = o[2 * j + u][h] + add;
-          red[warp][2 * c + h][32 * j + 4 * i + 2 * u + 1] = o[2 * j + u][2 + h] + add;
+          red[warp][2 * c + h][32 * j + 4 * i + 2 * u] = at.o[2 * j + u][h] * at.kUnit1 * unit + add;
+          red[warp][2 * c + h][32 * j + 4 * i + 2 * u + 1] =
+              at.o[2 * j + u][2 + h] * (at.kUnit1 * at.kOdd) * unit + add;
         }
       }
     }
     __syncthreads();
-    for (int at = threadIdx.x; at < ng * D; at += kThreads) {
-      const int hh = at / D, e = at - hh * D;
+    for (int x = threadIdx.x; x < ng * D; x += kThreads) {
+      const int hh = x / D, e = x - hh * D;
       float mx = -INFINITY;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, red[w][hh][D]);
@@ -330,7 +604,7 @@ q4_decode_kernel(Q4Problem p) {
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         // A warp without rows has m = -inf, l = acc = 0.
-        const float f = red[w][hh][D] == -INFINITY ? 0.f : exp2f(red[w][hh][D] - mx);
+        const float f = red[w][hh][D] == -INFINITY ? 0.f : exp2_approx(red[w][hh][D] - mx);
         ls = fmaf(red[w][hh][D + 1], f, ls);
         as = fmaf(red[w][hh][e], f, as);
       }
@@ -353,12 +627,12 @@ q4_decode_kernel(Q4Problem p) {
     const float* zv = p.z + (size_t)bh * D;
     const float* Mh = p.M + (size_t)bh * D * D;
     float* ret = p.ret + head0 * (D + 1);
-    if (warp < ng) {
+    for (int hh = warp; hh < ng; hh += kWarps) {
       float dp = 0.f;
 #pragma unroll
-      for (int e = 0; e < E; ++e) dp = fmaf(sq[warp][lane + 32 * e], zv[lane + 32 * e], dp);
+      for (int e = 0; e < E; ++e) dp = fmaf(sq[hh][lane + 32 * e], zv[lane + 32 * e], dp);
       dp = warp_sum(dp);
-      if (lane == 0) ret[(size_t)warp * (D + 1) + D] = dp;
+      if (lane == 0) ret[(size_t)hh * (D + 1) + D] = dp;
     }
     float acc[kHeads][E];
 #pragma unroll
@@ -402,15 +676,15 @@ q4_decode_kernel(Q4Problem p) {
   __syncthreads();
   if (!last) return;
   __threadfence();  // every other CTA's writes of this group are visible
-  if (warp < ng) {
-    // Warp w merges head w's partials, in chunk order; lane l columns l + 32 e.
-    const float* part = p.part + (head0 + warp) * p.nsplit * (D + 2);
-    const float* ret = p.ret + (head0 + warp) * (D + 1);
+  for (int hh = warp; hh < ng; hh += kWarps) {
+    // A warp merges a head's partials, in chunk order; lane l columns l + 32 e.
+    const float* part = p.part + (head0 + hh) * p.nsplit * (D + 2);
+    const float* ret = p.ret + (head0 + hh) * (D + 1);
     float num[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) num[e] = __ldcg(ret + lane + 32 * e);
     const float den = __ldcg(ret + D);
-    const float gm = gate_sigmoid(p.beta[hq0 + warp]);
+    const float gm = gate_sigmoid(p.beta[hq0 + hh]);
     float mx = -INFINITY, ls = 0.f, as[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) as[e] = 0.f;
@@ -429,20 +703,20 @@ q4_decode_kernel(Q4Problem p) {
       float nm = mx;
 #pragma unroll
       for (int u = 0; u < kU; ++u) nm = fmaxf(nm, mc[u]);
-      const float corr = exp2f(mx - nm);  // 0 for the first partials
+      const float corr = exp2_approx(mx - nm);  // 0 for the first partials
       ls *= corr;
 #pragma unroll
       for (int e = 0; e < E; ++e) as[e] *= corr;
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
-        const float f = exp2f(mc[u] - nm);  // 0 past the last partial
+        const float f = exp2_approx(mc[u] - nm);  // 0 past the last partial
         ls = fmaf(lc[u], f, ls);
 #pragma unroll
         for (int e = 0; e < E; ++e) as[e] = fmaf(ac[u][e], f, as[e]);
       }
       mx = nm;
     }
-    T* out = static_cast<T*>(p.out_t) + (head0 + warp) * D;
+    T* out = static_cast<T*>(p.out_t) + (head0 + hh) * D;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       const float a_mem = den != 0.f ? num[e] / den : 0.f;
@@ -452,81 +726,77 @@ q4_decode_kernel(Q4Problem p) {
   if (threadIdx.x == 0) *ctr = 0u;  // ready for the next step
 }
 
-// Rows of k and v [B, H_kv, n, D] into the buffers from row pos[b] on: one
-// warp per row and buffer.
+// Rows of k and v [B, H_kv, n, D] into the buffers from row pos[b] on.  A
+// thread takes 8 channels (16 bytes of bf16): 4 neighbours hold a group and
+// agree on its range by two exchanges, and each has whole words of the layout.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) q4_append_kernel(Q4Problem p, int n) {
-  const long long unit = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  const long long total = (long long)p.B * p.H_kv * n;
-  if (unit >= total) return;
-  const long long bh = unit / n;
-  const int t = (int)(unit - bh * n);
+  constexpr int PR = D / 8;  // threads per row
+  const int bh = blockIdx.y;
   const int pos = p.pos[bh / p.H_kv];
   if (pos < 0 || pos > p.S - n) {
-    if (pos != -1 && lane == 0) atomicOr(p.status, kStatusRange);
+    if (pos != -1 && threadIdx.x == 0) atomicOr(p.status, kStatusRange);
     return;
   }
+  const unsigned t = blockIdx.x * (kThreads / PR) + threadIdx.x / PR, w = threadIdx.x % PR;
+  const bool active = t < (unsigned)n;
+  const bool key = blockIdx.z == 0;
+  const T* src = static_cast<const T*>(key ? p.k_t : p.v_t) + ((size_t)bh * n + t) * D + 8 * w;
+  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (active) load8(src, v);
   const size_t row = (size_t)bh * p.S + pos + t;
-  if (blockIdx.y == 0)
-    store_row<T, D, true>(static_cast<const T*>(p.k_t) + unit * D, p.k_codes + row * (D / 2),
-                          p.k_scale + row * (D / 16), lane);
+  if (key)
+    store_group<D, true>(v, w, p.k_codes + row * (D / 2), p.k_scale + row * (D / 16), active);
   else
-    store_row<T, D, false>(static_cast<const T*>(p.v_t) + unit * D, p.v_codes + row * (D / 2),
-                           p.v_scale + row * (D / 16), lane);
+    store_group<D, false>(v, w, p.v_codes + row * (D / 2), p.v_scale + row * (D / 16), active);
 }
 
-// The values of rows 0..n-1 as k and v [B, H_kv, n, D]: a thread takes 8
-// channels (a key word) or 4 (a value halfword) of a row.
+// The values of rows 0..n-1 as k and v [B, H_kv, n, D]: a thread writes 8
+// channels (one key word, two value halfwords).
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) q4_read_kernel(Q4Problem p, int n, T* k, T* v) {
-  constexpr int NJ = D / 32;
-  const bool key = blockIdx.y == 0;
-  const int per_row = key ? D / 8 : D / 4;
-  const long long total = (long long)p.B * p.H_kv * n * per_row;
-  for (long long at = (long long)blockIdx.x * kThreads + threadIdx.x; at < total;
-       at += (long long)gridDim.x * kThreads) {
-    const long long unit = at / per_row;
-    const int w = (int)(at - unit * per_row);  // word of the row: channels 8w.. or 4w..
-    const long long bh = unit / n;
-    const size_t row = (size_t)bh * p.S + (unit - bh * n);
-    const int j = key ? w / 4 : w / 8;
-    const __nv_bfloat162 par =
-        reinterpret_cast<const __nv_bfloat162*>((key ? p.k_scale : p.v_scale) + row * (D / 16))[j];
-    const float s = __low2float(par), m = __high2float(par);
-    T* dst = (key ? k : v) + unit * D + (key ? 8 : 4) * w;
-    if (key) {
-      const uint32_t word = reinterpret_cast<const uint32_t*>(p.k_codes + row * (D / 2))[(w & 3) * NJ + j];
+  constexpr int NJ = D / 32, PR = D / 8;
+  const int bh = blockIdx.y;
+  const bool key = blockIdx.z == 0;
+  const unsigned t = blockIdx.x * (kThreads / PR) + threadIdx.x / PR, w = threadIdx.x % PR;
+  if (t >= (unsigned)n) return;
+  const size_t row = (size_t)bh * p.S + t;
+  const int j = w >> 2, c = w & 3;
+  const __nv_bfloat162 par =
+      reinterpret_cast<const __nv_bfloat162*>((key ? p.k_scale : p.v_scale) + row * (D / 16))[j];
+  const float s = __low2float(par), m = __high2float(par);
+  float out[8];
+  if (key) {
+    const uint32_t word = reinterpret_cast<const uint32_t*>(p.k_codes + row * (D / 2))[c * NJ + j];
 #pragma unroll
-      for (int o = 0; o < 8; ++o)
-        dst[o] = from_f32<T>(fmaf(s, (float)((word >> ((o & 1) ? 2 * o + 14 : 2 * o)) & 15u), m));
-    } else {
-      const uint32_t half =
-          reinterpret_cast<const unsigned short*>(p.v_codes + row * (D / 2))[(w & 7) * NJ + j];
+    for (int o = 0; o < 8; ++o) out[o] = fmaf(s, (float)((word >> ((o & 1) ? 2 * o + 14 : 2 * o)) & 15u), m);
+  } else {
+    const unsigned short* halves = reinterpret_cast<const unsigned short*>(p.v_codes + row * (D / 2));
+    const uint32_t pair = halves[2 * c * NJ + j] | (uint32_t)halves[(2 * c + 1) * NJ + j] << 16;
 #pragma unroll
-      for (int t = 0; t < 4; ++t) dst[t] = from_f32<T>(fmaf(s, (float)((half >> (4 * t)) & 15u), m));
-    }
+    for (int o = 0; o < 8; ++o) out[o] = fmaf(s, (float)((pair >> (4 * o)) & 15u), m);
   }
+  store8((key ? k : v) + ((size_t)bh * n + t) * D + 8 * w, out);
 }
 
 template <typename T, int D>
 cudaError_t launch(const Q4Problem& p, Q4What what, int n, void* k, void* v, cudaStream_t st) {
-  const long long rows = (long long)p.B * p.H_kv * n;
+  const dim3 rows((unsigned)(((long long)n * (D / 8) + kThreads - 1) / kThreads), p.B * p.H_kv, 2);
   switch (what) {
     case Q4What::kStep: {
       const int g = p.H_q / p.H_kv;
-      q4_decode_kernel<T, D><<<dim3(p.nsplit + 1, p.B * p.H_kv, (g + kHeads - 1) / kHeads), kThreads, 0, st>>>(p);
+      constexpr int ring = kWarps * Ring<D>::kStages * Ring<D>::kSlot, sums = kWarps * kHeads * (D + 2) * 4;
+      constexpr int bytes = ring > sums ? ring : sums;
+      cudaError_t e = cudaFuncSetAttribute(q4_decode_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+      if (e != cudaSuccess) return e;
+      q4_decode_kernel<T, D>
+          <<<dim3(p.nsplit + 1, p.B * p.H_kv, (g + kHeads - 1) / kHeads), kThreads, bytes, st>>>(p);
       break;
     }
-    case Q4What::kAppend:
-      q4_append_kernel<T, D><<<dim3((unsigned)((rows + kWarps - 1) / kWarps), 2), kThreads, 0, st>>>(p, n);
+    case Q4What::kAppend: q4_append_kernel<T, D><<<rows, kThreads, 0, st>>>(p, n); break;
+    case Q4What::kRead:
+      q4_read_kernel<T, D><<<rows, kThreads, 0, st>>>(p, n, static_cast<T*>(k), static_cast<T*>(v));
       break;
-    case Q4What::kRead: {
-      const long long blocks = (rows * (D / 8) + kThreads - 1) / kThreads;
-      const unsigned grid = (unsigned)(blocks < kSMs * 32 ? blocks : kSMs * 32);
-      q4_read_kernel<T, D><<<dim3(grid, 2), kThreads, 0, st>>>(p, n, static_cast<T*>(k), static_cast<T*>(v));
-      break;
-    }
   }
   return cudaGetLastError();
 }
@@ -549,7 +819,7 @@ int q4_head_chunks(int g) { return (g + kHeads - 1) / kHeads; }
 // leave about four waves of resident CTAs (two per SM), at most 16 units.
 int q4_chunk_rows(long long groups, int S) {
   const long long units = groups * ((S + kUnit - 1) / kUnit);
-  long long n = units / (kSMs * 2 * 4);
+  long long n = units / (kSMs * QB * QW);
   n = n < 1 ? 1 : n > 16 ? 16 : n;
   return (int)n * kUnit;
 }
