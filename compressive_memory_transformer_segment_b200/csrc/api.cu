@@ -1070,7 +1070,6 @@ Q4Problem q4_problem(const infini_dims_t* d, int seg_len, const CacheQ4& c) {
 
 // Workspace of a 4-bit decode step: [tickets | attention partials | retrieval].
 struct Q4Layout {
-  int chunk, nsplit;
   size_t part, ret, total;
 };
 
@@ -1081,10 +1080,8 @@ int q4_layout(const infini_dims_t* d, int seg_len, Q4Layout* lay) {
     return INFINI_ERR_UNSUPPORTED;
   const int zc = q4_head_chunks(d->H_q / d->H_kv);
   const size_t BHq = (size_t)d->B * d->H_q, dd = d->d_k;
-  lay->chunk = q4_chunk_rows((long long)d->B * d->H_kv * zc, seg_len);
-  lay->nsplit = (seg_len + lay->chunk - 1) / lay->chunk;
   lay->part = align_up((size_t)d->B * d->H_kv * zc * 4);
-  lay->ret = align_up(lay->part + BHq * lay->nsplit * (dd + 2) * 4);
+  lay->ret = align_up(lay->part + q4_partials(d->B, d->H_q, d->H_kv, seg_len) * (dd + 2) * 4);
   lay->total = align_up(lay->ret + BHq * (dd + 1) * 4);
   return INFINI_OK;
 }
@@ -1245,7 +1242,6 @@ int infini_attn_decode_step_q4(const void* q_t, const void* k_t, const void* v_t
   p.ctr = reinterpret_cast<unsigned int*>(ws);
   p.part = reinterpret_cast<float*>(ws + lay.part);
   p.ret = reinterpret_cast<float*>(ws + lay.ret);
-  p.chunk = lay.chunk; p.nsplit = lay.nsplit;
   cudaError_t e = launch_q4(p, Q4What::kStep, 1, nullptr, nullptr, st);
   if (owned) {
     cudaError_t f = cudaFreeAsync(ws, st);

@@ -25,11 +25,12 @@
 // per row (see the header), so rows go from global memory to the tensor cores
 // without shared memory; the next 16 rows are loaded while these are used.
 //
-// Grid: CTA 0 of a (batch row, KV head, chunk of 8 query heads) reads the
-// memory (sigma(q) M, sigma(q) z), the others up to `chunk` rows each; the
-// last one of them to finish (a ticket) merges and writes the output.  The
-// number of rows is read from device memory, so one captured launch serves
-// every position.
+// Grid: the rows of all (stream, KV head, chunk of 8 query heads) are shared out
+// in equal parts over as many CTAs as the GPU holds, whatever the streams'
+// lengths (read from device memory: one captured launch serves every
+// position); one more CTA each reads the memory (sigma(q) M, sigma(q) z).  The
+// last of a head chunk's CTAs to finish (a ticket) merges their partials in
+// order and writes the output.  No CTA waits for another.
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -40,20 +41,15 @@ namespace infini {
 
 namespace {
 
-#ifndef QT
-#define QT 256
-#endif
-#ifndef QB
-#define QB 2
-#endif
-#ifndef QW
-#define QW 4
-#endif
-constexpr int kThreads = QT;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kHeads = 8;               // query heads of a CTA (columns of a product)
 constexpr int kUnit = kWarps * 16;      // rows a CTA takes at a time
 constexpr int kSMs = 148;
+#ifndef QB
+#define QB 3
+#endif
+constexpr int kResident = QB;  // CTAs per SM (bf16 heads; two for fp32 ones)
 
 template <int BYTES> struct RawBytes;
 template <> struct RawBytes<2> { using type = unsigned short; };
@@ -205,6 +201,9 @@ struct Tile {
   Raw<D / 8> k[2];
   Raw<D / 8> kp[2], vp[2];
   Raw<D / 16> v[4];
+  // Minima (scales) of rows k_row(i), + 8 in two groups, as A fragments: groups
+  // 2 (c & 1) and the next for d = 128, 0 and 1 for 64, 0 and 0 for 32.
+  uint32_t kmin[2], kcen[2];
 };
 
 // A warp's ring of tiles in shared memory, filled by asynchronous copies: the
@@ -214,10 +213,11 @@ template <int D>
 struct Ring {
   static constexpr int kCodes = 16 * (D / 2), kParams = 16 * (D / 8);  // bytes of 16 rows
   static constexpr int kSlot = 2 * kCodes + 2 * kParams;
-  #ifndef QS
-#define QS 4
-#endif
+    #ifdef QS
   static constexpr int kStages = QS;
+#else
+  static constexpr int kStages = 4;
+#endif
   uint8_t* smem;
   const uint8_t *k, *v, *par;  // this lane's source in the chunk's first 16 rows
   int n, lane;                 // rows of the chunk
@@ -230,34 +230,46 @@ struct Ring {
     par = reinterpret_cast<const uint8_t*>(lane < 16 ? p.k_scale : p.v_scale) + (row0 + (lane & 15)) * (D / 8);
   }
   template <int BYTES>
-  __device__ __forceinline__ static void copy(uint8_t* dst, const uint8_t* src, bool in) {
-    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
-    const int size = in ? BYTES : 0;  // the rest is filled with zeros
+  __device__ __forceinline__ static void copy(uint32_t to, const uint8_t* src) {
     if constexpr (BYTES == 16)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src), "r"(size) : "memory");
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(src) : "memory");
     else
-      asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to), "l"(src), "n"(BYTES), "r"(size)
-                   : "memory");
+      asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(src), "n"(BYTES) : "memory");
   }
-  // Starts the copy of rows r .. r + 15; rows from n on become zeros, whatever
-  // the buffer holds there (their addresses are not read).
-  __device__ __forceinline__ void fill(int slot, int r) const {
-    uint8_t* s = smem + slot * kSlot;
+  // BYTES zeros instead of a copy.
+  template <int BYTES>
+  __device__ __forceinline__ static void zero(uint32_t to) {
+#pragma unroll
+    for (int e = 0; e < BYTES; e += 4) asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + e), "r"(0) : "memory");
+  }
+  template <int BYTES, bool FULL>
+  __device__ __forceinline__ static void piece(uint32_t to, const uint8_t* src, bool in) {
+    if (FULL || in) copy<BYTES>(to, src);
+    else zero<BYTES>(to);
+  }
+  template <bool FULL>
+  __device__ __forceinline__ void fill_rows(int slot, int r) const {
+    const uint32_t s = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + slot * kSlot + lane * 16;
     const size_t off = (size_t)r * (D / 2);
     if constexpr (D == 32) {
-      const bool in = r + (lane & 15) < n;
-      copy<16>(s + lane * 16, (lane < 16 ? k : v) + (in ? off : 0), in);
+      piece<16, FULL>(s, (lane < 16 ? k : v) + off, r + (lane & 15) < n);
     } else {
       constexpr int PR = D / 32;  // pieces per row
+      const uint8_t *ks = k + off, *vs = v + off;
 #pragma unroll
       for (int e = 0; e < kCodes / 512; ++e) {
         const bool in = r + (lane + 32 * e) / PR < n;
-        copy<16>(s + (lane + 32 * e) * 16, k + (in ? off + 512 * e : 0), in);
-        copy<16>(s + kCodes + (lane + 32 * e) * 16, v + (in ? off + 512 * e : 0), in);
+        piece<16, FULL>(s + 512 * e, ks + 512 * e, in);
+        piece<16, FULL>(s + kCodes + 512 * e, vs + 512 * e, in);
       }
     }
-    const bool in = r + (lane & 15) < n;
-    copy<D / 8>(s + 2 * kCodes + lane * (D / 8), par + (in ? (size_t)r * (D / 8) : 0), in);
+    piece<D / 8, FULL>(s + 2 * kCodes - lane * (16 - D / 8), par + (size_t)r * (D / 8), r + (lane & 15) < n);
+  }
+  // Starts the copy of rows r .. r + 15; rows from n on become zeros, whatever
+  // the buffer holds there.
+  __device__ __forceinline__ void fill(int slot, int r) const {
+    if (r + 16 <= n) fill_rows<true>(slot, r);
+    else fill_rows<false>(slot, r);
   }
   __device__ __forceinline__ static void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
   // Waits until at most kStages - 1 groups of this lane are in flight.
@@ -272,6 +284,13 @@ struct Ring {
       t.k[e].load(s + (kr + 8 * e) * (D / 2) + c * (D / 8));
       t.kp[e].load(s + 2 * kCodes + (kr + 8 * e) * (D / 8));
       t.vp[e].load(s + 2 * kCodes + kParams + (kr + 8 * e) * (D / 8));
+      uint32_t a = t.kp[e].word(0), b = t.kp[e].word(D / 32 > 1 ? 1 : 0);
+      if constexpr (D == 128) {
+        const uint2 w = *reinterpret_cast<const uint2*>(s + 2 * kCodes + (kr + 8 * e) * 16 + (c & 1) * 8);
+        a = w.x; b = w.y;
+      }
+      t.kmin[e] = __byte_perm(a, b, 0x7632);
+      t.kcen[e] = __byte_perm(a, b, 0x5410);
       t.v[2 * e].load(s + kCodes + (c + 8 * e) * (D / 2) + i * (D / 16));
       t.v[2 * e + 1].load(s + kCodes + (4 + (c ^ 1) + 8 * e) * (D / 2) + i * (D / 16));
     }
@@ -350,14 +369,18 @@ struct Attention {
   static constexpr float kUnit1 = kExact ? 1.f : 0x1p24f;        // of a product with q, or with q - 8
   static constexpr float kOdd = kExact ? 1.f : 0.0625f;          // second and fourth codes
   static constexpr float kCenter = kExact ? 8.f : 0.f;
+  static constexpr float kLead = 7.f;
   uint32_t qf[NJ][NP][4];  // queries of head i as B fragments, times 2^e (pairs 1, 3: kOdd of that)
-  float qsum[NJ][2];       // sum of a head's scaled query over each group, in units of a code
+  // Sums of head i's scaled query over each group, in units of a code, as a B
+  // operand of bf16 parts: index 4 part + group (d = 128), 2 part + group (64),
+  // 2 part (32) along the minima.
+  uint32_t qs[2], qc[2];   // (qc: times kCenter)
   float f1, f2[2];         // log2(e) / sqrt(d) kUnit1, 2^-e: scores to powers of two
-  float m[2], l[2];        // running maximum; sum over this lane's rows
+  float m[2], l[2];        // reference of the powers; their sum over this lane's rows
   float o[2 * NJ][4];      // O^T without the minima, times 2^-pe / kUnit1 (rows i + 8: over kOdd too)
   float omin[NJ][2];       // sum of p (minimum + kCenter scale) over this lane's rows
   int pe;                  // p scale 2^-pe is what the products get
-  uint32_t limit;          // bf16 bits of the largest scale that 2^-pe holds below 2^15
+  uint32_t limit;          // bf16 bits of the largest scale that 2^-pe takes to 2^8
 
   // q_t: this KV head's first query; ng: heads of it that exist.
   template <typename T>
@@ -377,6 +400,7 @@ struct Attention {
     // The largest element goes to 2^14 .. 2^15.
     const int e = min(14 + 127 - (__float_as_int(top) >> 23), 100);
     const float up = pow2(e);
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
       float s = 0.f;
@@ -387,8 +411,7 @@ struct Attention {
       }
       s += __shfl_xor_sync(0xffffffffu, s, 1);
       s += __shfl_xor_sync(0xffffffffu, s, 2);
-      qsum[j][0] = __shfl_sync(0xffffffffu, s, 8 * c) * (1.f / kUnit1);
-      qsum[j][1] = __shfl_sync(0xffffffffu, s, 8 * c + 4) * (1.f / kUnit1);
+      sum[j] = s * (1.f / kUnit1);
 #pragma unroll
       for (int k = 2; k < 8; k += 4) {
         x[j][k] *= kOdd;
@@ -402,6 +425,27 @@ struct Attention {
 #pragma unroll
       for (int k = 0; k < 4; ++k) o[2 * j][k] = o[2 * j + 1][k] = 0.f;
     }
+    // This lane's indexes along the minima: 2c, 2c + 1 (b0), 2c + 8, 2c + 9 (b1).
+    {
+      const bool upper = NJ == 4 && (c & 1);
+      float lo = upper ? sum[2] : sum[0], hi = upper ? sum[3] : sum[1];
+      uint32_t part[3];
+#pragma unroll
+      for (int k = 0; k < 3; ++k) part[k] = split_bf16(lo, hi);
+      if constexpr (NJ == 4) {
+        qs[0] = c < 2 ? part[0] : part[1];
+        qs[1] = c < 2 ? part[2] : 0u;
+      } else {
+        qs[0] = c == 0 ? part[0] : c == 1 ? part[1] : c == 2 ? part[2] : 0u;
+        qs[1] = 0u;
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&qs[k]),
+                                         __floats2bfloat162_rn(kCenter, kCenter));  // a power of two
+        qc[k] = *reinterpret_cast<const uint32_t*>(&v);
+      }
+    }
     f1 = rsqrtf((float)D) * 1.4426950408889634f * kUnit1;
     f2[0] = pow2(-__shfl_sync(0xffffffffu, e, 8 * c));
     f2[1] = pow2(-__shfl_sync(0xffffffffu, e, 8 * c + 4));
@@ -411,23 +455,48 @@ struct Attention {
     limit = 0;
   }
 
+  // The reference becomes the maximum so far.
+  __device__ __forceinline__ void rebase(const float (&x)[4]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float mn = fmaxf(m[h], column_max(fmaxf(x[h], x[2 + h])));
+      const float corr = exp2_approx(m[h] - mn);  // 0 for the first rows
+      m[h] = mn;
+      l[h] *= corr;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        omin[j][h] *= corr;
+        o[2 * j][h] *= corr; o[2 * j][2 + h] *= corr;
+        o[2 * j + 1][h] *= corr; o[2 * j + 1][2 + h] *= corr;
+      }
+    }
+  }
+
   // A scale beyond the limit: the unit moves so that the largest of these rows
-  // lies at 2^7 .. 2^8 (the first rows set it so).
+  // lies at 1 .. 2 (the first rows set it so).  With probabilities up to
+  // 2^kLead there is room for scales 2^7 times as large before the next move.
   __device__ __forceinline__ void raise(uint32_t top) {
     top = __reduce_max_sync(0xffffffffu, top);
-    const int to = max(min((int)(top >> 7), 255) - 127 - 7, -120);
+    if (top <= limit) return;
+    const int to = max(min((int)(top >> 7), 255) - 127, -120);
     const float down = exp2f((float)(pe - to));
 #pragma unroll
     for (int j = 0; j < 2 * NJ; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[j][e] *= down;
     pe = to;
-    limit = min(to + 15 + 127, 255) << 7;
+    limit = min(to + 8 + 127, 255) << 7;
   }
 
+  // FULL: all 16 rows count; else rows k_row(i) (in0) and + 8 (in1) of a lane do
+  // or do not.
+  template <bool FULL>
   __device__ __forceinline__ void step(const Tile<D>& t, bool in0, bool in1) {
     // Scores of rows i (s[0], s[1]) and i + 8 (s[2], s[3]).
+    // The minima's share first: (minima of a row) times (sums of the queries).
     float s[4] = {0.f, 0.f, 0.f, 0.f};
+    mma_bf16(s, t.kmin[0], t.kmin[1], t.kmin[0], t.kmin[1], qs[0], qs[1]);
+    if constexpr (kExact) mma_bf16(s, t.kcen[0], t.kcen[1], t.kcen[0], t.kcen[1], qc[0], qc[1]);
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
       uint32_t fa[4], fb[4];
@@ -444,39 +513,30 @@ struct Attention {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const float sc = t.kp[e].scale(j);
-        const float mn = kExact ? fmaf(kCenter, sc, t.kp[e].minimum(j)) : t.kp[e].minimum(j);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) s[2 * e + h] = fmaf(sc, d[2 * e + h], fmaf(mn, qsum[j][h], s[2 * e + h]));
+        for (int h = 0; h < 2; ++h) s[2 * e + h] = fmaf(sc, d[2 * e + h], s[2 * e + h]);
       }
     }
-    float pr[4], corr[2];
+    // Powers of two relative to a reference m, at most 2^kLead of it: a maximum
+    // is taken over the warp only when a score leaves that room (and by the
+    // first rows), not for every tile.
+    float x[4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float s0 = in0 ? s[h] * f1 * f2[h] : -INFINITY, s1 = in1 ? s[2 + h] * f1 * f2[h] : -INFINITY;
-      const float mn = fmaxf(m[h], column_max(fmaxf(s0, s1)));
-      corr[h] = exp2_approx(m[h] - mn);  // 0 for the first rows
-      m[h] = mn;
-      pr[h] = exp2_approx(s0 - mn);
-      pr[2 + h] = exp2_approx(s1 - mn);
-      l[h] = fmaf(l[h], corr[h], pr[h] + pr[2 + h]);
-    }
-    // The maximum rarely moves after the first rows (written so that a NaN
-    // rescales too).
-    if (__any_sync(0xffffffffu, !(corr[0] == 1.f && corr[1] == 1.f))) {
-#pragma unroll
-      for (int j = 0; j < NJ; ++j)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          omin[j][h] *= corr[h];
-          o[2 * j][h] *= corr[h]; o[2 * j][2 + h] *= corr[h];
-          o[2 * j + 1][h] *= corr[h]; o[2 * j + 1][2 + h] *= corr[h];
-        }
-    }
+    for (int e = 0; e < 4; ++e) x[e] = FULL || (e < 2 ? in0 : in1) ? s[e] * f1 * f2[e & 1] : -INFINITY;
     uint32_t top = 0;
 #pragma unroll
     for (int j = 0; j < NJ; ++j) top = __vimax3_u16x2(top, t.vp[0].word(j), t.vp[1].word(j));
     top &= 0xffffu;  // the scales are the low halves
-    if (__any_sync(0xffffffffu, top > limit)) raise(top);
+    const float over = fmaxf(fmaxf(x[0], x[2]) - m[0], fmaxf(x[1], x[3]) - m[1]);
+    if (__any_sync(0xffffffffu, over > kLead || top > limit)) {
+      rebase(x);
+      raise(top);
+    }
+    float pr[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) pr[e] = exp2_approx(x[e] - m[e & 1]);
+    l[0] += pr[0] + pr[2];
+    l[1] += pr[1] + pr[3];
     const float p2 = pow2(-pe);
     float w[4];
 #pragma unroll
@@ -509,221 +569,338 @@ struct Attention {
   }
 };
 
+// Units of p.unit rows of stream b (0: idle).
+__device__ __forceinline__ uint32_t stream_units(const Q4Problem& p, int b) {
+  const int pos = p.pos[b];
+  return pos >= 0 && pos < p.S ? pos / p.unit + 1 : 0;
+}
+
+// How the units of all segments are shared out.  A segment is what one (stream,
+// KV head, chunk of 8 query heads) attends to; segments lie one after another
+// (stream by stream, segs of equal length each), and CTA k of `ctas` takes
+// units [k U / ctas, (k + 1) U / ctas) of the U in all: equal work whatever
+// the streams' lengths are.  (A launch whose units are no more than its CTAs has
+// one unit per CTA: none then has two segments.)
+struct Share {
+  uint32_t units, ctas;
+  __device__ __forceinline__ uint32_t first(uint32_t k) const {
+    return (uint32_t)((unsigned long long)k * units / ctas);
+  }
+  __device__ __forceinline__ uint32_t owner(uint32_t u) const {
+    return (uint32_t)(((unsigned long long)(u + 1) * ctas + units - 1) / units) - 1;
+  }
+};
+
+// Adds up the streams' units (the whole CTA calls it): the total, and the
+// stream and its first unit that `unit_of(total)` lies in, or, for by_stream,
+// of stream `unit_of(total)`.
+template <typename F>
+__device__ __forceinline__ uint32_t locate(const Q4Problem& p, uint32_t segs, bool by_stream, F&& unit_of,
+                                           uint32_t& stream, uint32_t& start) {
+  __shared__ uint32_t sums[kWarps], found[2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int per = (p.B + kThreads - 1) / kThreads, b0 = min((int)threadIdx.x * per, p.B), b1 = min(b0 + per, p.B);
+  uint32_t mine = 0;
+  for (int b = b0; b < b1; ++b) mine += stream_units(p, b) * segs;
+  uint32_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) sums[warp] = incl;
+  __syncthreads();
+  uint32_t total = 0, at = incl - mine;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) at += sums[w];
+    total += sums[w];
+  }
+  const uint32_t want = unit_of(total);
+  for (int b = b0; b < b1; ++b) {
+    const uint32_t n = stream_units(p, b) * segs;
+    if (by_stream ? b == (int)want : want >= at && want < at + n) {
+      found[0] = b;
+      found[1] = at;
+    }
+    at += n;
+  }
+  __syncthreads();
+  stream = found[0];
+  start = found[1];
+  return total;
+}
+
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, Parts<T>::n == 1 ? QB : 1)
+__global__ void __launch_bounds__(kThreads, Parts<T>::n == 1 ? kResident : 2)
 q4_decode_kernel(Q4Problem p) {
-  constexpr int NJ = D / 32;           // groups
-  constexpr int E = D / 32;            // channels per lane in the merges
+  constexpr int E = D / 32;  // channels per lane in the merges
   constexpr int NP = Parts<T>::n;
+  using R = Ring<D>;
   extern __shared__ __align__(16) uint8_t smem[];
   float(*red)[kHeads][D + 2] = reinterpret_cast<float(*)[kHeads][D + 2]>(smem);  // [kWarps]
   __shared__ int last;
 
-  const int bh = blockIdx.y;
-  const int b = bh / p.H_kv, hk = bh - b * p.H_kv;
-  const int pos = p.pos[b];
-  if (pos < 0 || pos >= p.S) {  // an idle stream; nothing of it is touched
-    if (pos != -1 && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.status, kStatusRange);
-    return;
-  }
-  const int nch = pos / p.chunk + 1;
-  if ((int)blockIdx.x > nch) return;
-  const int g = p.H_q / p.H_kv;
-  const int hq0 = hk * g + blockIdx.z * kHeads;
-  const int ng = min(kHeads, g - (int)blockIdx.z * kHeads);
+  const int g = p.H_q / p.H_kv, zc = (g + kHeads - 1) / kHeads;
+  const uint32_t segs = (uint32_t)(p.H_kv * zc);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const size_t head0 = (size_t)b * p.H_q + hq0;
-  const T* q_t = static_cast<const T*>(p.q_t) + head0 * D;
+  const int i = lane >> 2, c = lane & 3;
+  // The retrievals come first: they are short and every output waits for one.
+  const uint32_t retrievals = (uint32_t)p.B * segs;
+  const bool attend = blockIdx.x >= retrievals;
+  const uint32_t cta = blockIdx.x - retrievals;
 
-  if (blockIdx.x > 0) {
-    // ------------------------------------------------ attention partial
-    const int r0 = (blockIdx.x - 1) * p.chunk, r1 = min(r0 + p.chunk, pos + 1);
-    const int i = lane >> 2, c = lane & 3;
-    if (r1 == pos + 1) {
-      // This CTA's rows include the token's own: it is stored first (by every
-      // head chunk, the same bytes) and then read like any other.
-      const size_t row = (size_t)bh * p.S + pos;
-      if (warp == 0)
-        store_row<T, D, true>(static_cast<const T*>(p.k_t) + (size_t)bh * D, p.k_codes + row * (D / 2),
-                              p.k_scale + row * (D / 16), lane);
-      else if (warp == 1)
-        store_row<T, D, false>(static_cast<const T*>(p.v_t) + (size_t)bh * D, p.v_codes + row * (D / 2),
-                               p.v_scale + row * (D / 16), lane);
-      __syncthreads();
+  uint32_t b, off;  // stream, its first unit
+  Share share;
+  uint32_t u, u_end, seg;  // units of this CTA; segment of the stream
+  if (attend) {
+    share.units = locate(p, segs, false, [&](uint32_t total) {
+      share = {total, min((uint32_t)p.ctas, total)};
+      return cta < share.ctas ? share.first(cta) : 0u;
+    }, b, off);
+    if (cta >= share.ctas) return;
+    u = share.first(cta);
+    u_end = share.first(cta + 1);
+  } else {
+    const uint32_t stream = blockIdx.x / segs;
+    seg = blockIdx.x - stream * segs;
+    share.units = locate(p, segs, true, [&](uint32_t) { return stream; }, b, off);
+    share.ctas = min((uint32_t)p.ctas, share.units);
+    const int pos = p.pos[b];
+    if (pos < 0 || pos >= p.S) {  // an idle stream; nothing of it is touched
+      if (pos != -1 && seg == 0 && threadIdx.x == 0) atomicOr(p.status, kStatusRange);
+      return;
     }
-    const Ring<D> ring(p, smem + warp * Ring<D>::kStages * Ring<D>::kSlot, (size_t)bh * p.S + r0, r1 - r0, lane);
-#pragma unroll
-    for (int e = 0; e < Ring<D>::kStages; ++e) {
-      const int r = warp * 16 + e * kUnit;
-      if (r < ring.n) ring.fill(e, r);
-      ring.commit();
-    }
-    Attention<D, NP> at;
-    at.init(q_t, ng, lane);
-    const int kr = k_row(i);
-    int slot = 0;
-    for (int r = warp * 16; r < ring.n; r += kUnit) {
-      ring.wait();
-      __syncwarp();
-      Tile<D> t;
-      ring.read(t, slot);
-      __syncwarp();  // every lane has read the slot
-      const int ahead = r + Ring<D>::kStages * kUnit;
-      if (ahead < ring.n) ring.fill(slot, ahead);
-      ring.commit();
-      at.step(t, r + kr < ring.n, r + kr + 8 < ring.n);
-      slot = slot + 1 < Ring<D>::kStages ? slot + 1 : 0;
-    }
-    __syncthreads();  // the sums below lie where the rings were
-    // This warp's (max, sum, acc) of heads 2c, 2c + 1.
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      at.l[h] = column_sum(at.l[h]);
-      if (i == 0) {
-        red[warp][2 * c + h][D] = at.m[h];
-        red[warp][2 * c + h][D + 1] = at.l[h];
+    u = off;
+    u_end = off + 1;  // one turn of the loop
+  }
+
+  for (bool first = true; u < u_end; first = false) {
+    const int pos = p.pos[b];
+    const uint32_t n = pos / p.unit + 1;
+    if (attend) seg = (u - off) / n;
+    const uint32_t s0 = off + seg * n, s1 = s0 + n;  // the segment's units
+    const uint32_t e_unit = attend ? min(u_end, s1) : u_end;
+    const int hk = seg / zc, hq0 = hk * g + (seg - hk * zc) * kHeads;
+    const int ng = min(kHeads, (hk + 1) * g - hq0);
+    const size_t bh = (size_t)b * p.H_kv + hk;
+    const size_t head0 = (size_t)b * p.H_q + hq0;
+    const T* q_t = static_cast<const T*>(p.q_t) + head0 * D;
+    // Partials of a segment: of a CTA that has it whole, at the segment's own
+    // place; of others, at the CTA's (its first segment, or its last).
+    const uint32_t k_first = share.owner(s0), k_last = share.owner(s1 - 1);
+
+    if (attend) {
+      // ---------------------------------------------- attention partial
+      const int r0 = (u - s0) * p.unit;
+      const int r1 = (int)min((long long)(e_unit - s0) * p.unit, (long long)pos + 1);
+      if (r1 == pos + 1) {
+        // These rows include the token's own: it is stored first (by every
+        // head chunk, the same bytes) and then read like any other.
+        const size_t row = bh * p.S + pos;
+        if (warp == 0)
+          store_row<T, D, true>(static_cast<const T*>(p.k_t) + bh * D, p.k_codes + row * (D / 2),
+                                p.k_scale + row * (D / 16), lane);
+        else if (warp == 1)
+          store_row<T, D, false>(static_cast<const T*>(p.v_t) + bh * D, p.v_codes + row * (D / 2),
+                                 p.v_scale + row * (D / 16), lane);
+        __syncthreads();
       }
+      R ring(p, smem + warp * R::kStages * R::kSlot, bh * p.S + r0, r1 - r0, lane);
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        const float add = column_sum(at.omin[j][h]), unit = exp2f((float)at.pe);
+      for (int e = 0; e < R::kStages; ++e) {
+        const int r = warp * 16 + e * kUnit;
+        if (r < ring.n) ring.fill(e, r);
+        ring.commit();
+      }
+      Attention<D, NP> at;
+      at.init(q_t, ng, lane);
+      const int kr = k_row(i);
+      int slot = 0;
+      for (int r = warp * 16; r < ring.n; r += kUnit) {
+        ring.wait();
+        __syncwarp();
+        Tile<D> t;
+        ring.read(t, slot);
+        __syncwarp();  // every lane has read the slot
+        const int ahead = r + R::kStages * kUnit;
+        if (ahead < ring.n) ring.fill(slot, ahead);
+        ring.commit();
+        if (r + 16 <= ring.n)
+          at.template step<true>(t, true, true);
+        else
+          at.template step<false>(t, r + kr < ring.n, r + kr + 8 < ring.n);
+        slot = slot + 1 < R::kStages ? slot + 1 : 0;
+      }
+      __syncthreads();  // the sums below lie where the rings were
+      // This warp's (max, sum, acc) of heads 2c, 2c + 1.
+      const float unit = exp2f((float)at.pe);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          red[warp][2 * c + h][32 * j + 4 * i + 2 * u] = at.o[2 * j + u][h] * at.kUnit1 * unit + add;
-          red[warp][2 * c + h][32 * j + 4 * i + 2 * u + 1] =
-              at.o[2 * j + u][2 + h] * (at.kUnit1 * at.kOdd) * unit + add;
+      for (int h = 0; h < 2; ++h) {
+        at.l[h] = column_sum(at.l[h]);
+        if (i == 0) {
+          red[warp][2 * c + h][D] = at.m[h];
+          red[warp][2 * c + h][D + 1] = at.l[h];
+        }
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) {
+          const float add = column_sum(at.omin[j][h]);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float* to = &red[warp][2 * c + h][32 * j + 4 * i + 2 * k];
+            to[0] = at.o[2 * j + k][h] * at.kUnit1 * unit + add;
+            to[1] = at.o[2 * j + k][2 + h] * (at.kUnit1 * at.kOdd) * unit + add;
+          }
         }
       }
-    }
-    __syncthreads();
-    for (int x = threadIdx.x; x < ng * D; x += kThreads) {
-      const int hh = x / D, e = x - hh * D;
-      float mx = -INFINITY;
+      __syncthreads();
+      const size_t base = k_first == k_last ? head0 : (size_t)p.B * p.H_q + ((size_t)cta * 2 + !first) * kHeads;
+      for (int x = threadIdx.x; x < ng * D; x += kThreads) {
+        const int hh = x / D, e = x - hh * D;
+        float mx = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, red[w][hh][D]);
-      float ls = 0.f, as = 0.f;
+        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, red[w][hh][D]);
+        float ls = 0.f, as = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        // A warp without rows has m = -inf, l = acc = 0.
-        const float f = red[w][hh][D] == -INFINITY ? 0.f : exp2_approx(red[w][hh][D] - mx);
-        ls = fmaf(red[w][hh][D + 1], f, ls);
-        as = fmaf(red[w][hh][e], f, as);
+        for (int w = 0; w < kWarps; ++w) {
+          // A warp without rows has m = -inf, l = acc = 0.
+          const float f = red[w][hh][D] == -INFINITY ? 0.f : exp2_approx(red[w][hh][D] - mx);
+          ls = fmaf(red[w][hh][D + 1], f, ls);
+          as = fmaf(red[w][hh][e], f, as);
+        }
+        float* part = p.part + (base + hh) * (D + 2);
+        part[2 + e] = as;
+        if (e == 0) {
+          part[0] = mx;
+          part[1] = ls;
+        }
       }
-      float* part = p.part + ((head0 + hh) * p.nsplit + blockIdx.x - 1) * (D + 2);
-      part[2 + e] = as;
-      if (e == 0) {
-        part[0] = mx;
-        part[1] = ls;
+    } else {
+      // ---------------------------------------------- retrieval
+      // Warp w sums every kWarps-th group of 16 of M's rows, lane l columns
+      // l + 32 k.
+      float(*sq)[D] = reinterpret_cast<float(*)[D]>(smem);  // [kHeads][D], before the sums
+      for (int x = threadIdx.x; x < kHeads * D; x += kThreads) {
+        const int hh = x / D, e = x - hh * D;
+        sq[hh][e] = hh < ng ? elu1(to_f32<T>(q_t[(size_t)hh * D + e])) : 0.f;
       }
-    }
-  } else {
-    // ------------------------------------------------ retrieval
-    // Warp w sums M's rows [w D/8, (w+1) D/8), lane l columns l + 32 k.
-    float(*sq)[D] = reinterpret_cast<float(*)[D]>(&red[0][0][0]);  // [kHeads][D], before the sums
-    for (int at = threadIdx.x; at < kHeads * D; at += kThreads) {
-      const int hh = at / D, e = at - hh * D;
-      sq[hh][e] = hh < ng ? elu1(to_f32<T>(q_t[(size_t)hh * D + e])) : 0.f;
-    }
-    __syncthreads();
-    const float* zv = p.z + (size_t)bh * D;
-    const float* Mh = p.M + (size_t)bh * D * D;
-    float* ret = p.ret + head0 * (D + 1);
-    for (int hh = warp; hh < ng; hh += kWarps) {
-      float dp = 0.f;
+      __syncthreads();
+      const float* zv = p.z + bh * D;
+      const float* Mh = p.M + bh * D * D;
+      float* ret = p.ret + head0 * (D + 1);
+      for (int hh = warp; hh < ng; hh += kWarps) {
+        float dp = 0.f;
 #pragma unroll
-      for (int e = 0; e < E; ++e) dp = fmaf(sq[hh][lane + 32 * e], zv[lane + 32 * e], dp);
-      dp = warp_sum(dp);
-      if (lane == 0) ret[(size_t)hh * (D + 1) + D] = dp;
-    }
-    float acc[kHeads][E];
+        for (int e = 0; e < E; ++e) dp = fmaf(sq[hh][lane + 32 * e], zv[lane + 32 * e], dp);
+        dp = warp_sum(dp);
+        if (lane == 0) ret[(size_t)hh * (D + 1) + D] = dp;
+      }
+      float acc[kHeads][E];
 #pragma unroll
-    for (int hh = 0; hh < kHeads; ++hh)
+      for (int hh = 0; hh < kHeads; ++hh)
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[hh][e] = 0.f;
-    constexpr int kRowsPerWarp = D / kWarps;
+        for (int e = 0; e < E; ++e) acc[hh][e] = 0.f;
+      constexpr int kRowsPerWarp = D / kWarps;
 #pragma unroll 8
-    for (int k = 0; k < kRowsPerWarp; ++k) {
-      const int row = warp * kRowsPerWarp + k;
-      float mrow[E];
+      for (int k = 0; k < kRowsPerWarp; ++k) {
+        const int row = warp * kRowsPerWarp + k;
+        float mrow[E];
 #pragma unroll
-      for (int e = 0; e < E; ++e) mrow[e] = Mh[(size_t)row * D + lane + 32 * e];
+        for (int e = 0; e < E; ++e) mrow[e] = Mh[(size_t)row * D + lane + 32 * e];
 #pragma unroll
-      for (int hh = 0; hh < kHeads; ++hh) {
-        const float w = sq[hh][row];
+        for (int hh = 0; hh < kHeads; ++hh) {
+          const float w = sq[hh][row];
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[hh][e] = fmaf(w, mrow[e], acc[hh][e]);
+          for (int e = 0; e < E; ++e) acc[hh][e] = fmaf(w, mrow[e], acc[hh][e]);
+        }
+      }
+      __syncthreads();  // sq has been read
+#pragma unroll
+      for (int hh = 0; hh < kHeads; ++hh)
+#pragma unroll
+        for (int e = 0; e < E; ++e) red[warp][hh][lane + 32 * e] = acc[hh][e];
+      __syncthreads();
+      for (int x = threadIdx.x; x < ng * D; x += kThreads) {
+        const int hh = x / D, e = x - hh * D;
+        float num = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) num += red[w][hh][e];
+        ret[(size_t)hh * (D + 1) + e] = num;
       }
     }
-    __syncthreads();  // sq has been read
-#pragma unroll
-    for (int hh = 0; hh < kHeads; ++hh)
-#pragma unroll
-      for (int e = 0; e < E; ++e) red[warp][hh][lane + 32 * e] = acc[hh][e];
-    __syncthreads();
-    for (int at = threadIdx.x; at < ng * D; at += kThreads) {
-      const int hh = at / D, e = at - hh * D;
-      float num = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) num += red[w][hh][e];
-      ret[(size_t)hh * (D + 1) + e] = num;
-    }
-  }
 
-  // ------------------------------------------------ the last CTA finishes
-  __threadfence();  // this thread's workspace writes, before the ticket
-  __syncthreads();
-  unsigned int* ctr = p.ctr + (size_t)bh * gridDim.z + blockIdx.z;
-  if (threadIdx.x == 0) last = atomicAdd(ctr, 1u) == (unsigned int)nch;
-  __syncthreads();
-  if (!last) return;
-  __threadfence();  // every other CTA's writes of this group are visible
-  for (int hh = warp; hh < ng; hh += kWarps) {
-    // A warp merges a head's partials, in chunk order; lane l columns l + 32 e.
-    const float* part = p.part + (head0 + hh) * p.nsplit * (D + 2);
-    const float* ret = p.ret + (head0 + hh) * (D + 1);
-    float num[E];
+    // ------------------------------------------------ the last CTA finishes
+    __threadfence();  // this thread's workspace writes, before the ticket
+    __syncthreads();
+    unsigned int* ctr = p.ctr + (size_t)b * segs + seg;
+    if (threadIdx.x == 0) last = atomicAdd(ctr, 1u) == k_last - k_first + 1;
+    __syncthreads();
+    if (last) {
+      __threadfence();  // every other CTA's writes of this segment are visible
+      // Partial x of head hh (x = 0 .. k_last - k_first): only the first CTA of
+      // several may have had another segment before this one.
+      const bool later = k_first != k_last && share.first(k_first) != s0;
+      auto partial = [&](uint32_t x, int hh) {
+        const size_t at = k_first == k_last ? head0
+                                            : (size_t)p.B * p.H_q +
+                                                  ((size_t)(k_first + x) * 2 + (x == 0 && later)) * kHeads;
+        return p.part + (at + hh) * (D + 2);
+      };
+      const int np = k_last - k_first + 1;
+      for (int hh = warp; hh < ng; hh += kWarps) {
+        // A warp merges a head's partials, in CTA order; lane l columns l + 32 e.
+        const float* ret = p.ret + (head0 + hh) * (D + 1);
+        float num[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) num[e] = __ldcg(ret + lane + 32 * e);
-    const float den = __ldcg(ret + D);
-    const float gm = gate_sigmoid(p.beta[hq0 + hh]);
-    float mx = -INFINITY, ls = 0.f, as[E];
+        for (int e = 0; e < E; ++e) num[e] = __ldcg(ret + lane + 32 * e);
+        const float den = __ldcg(ret + D);
+        const float gm = gate_sigmoid(p.beta[hq0 + hh]);
+        float mx = -INFINITY, ls = 0.f, as[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) as[e] = 0.f;
-    constexpr int kU = 8;  // partials in flight
-    for (int c0 = 0; c0 < nch; c0 += kU) {
-      float mc[kU], lc[kU], ac[kU][E];
+        for (int e = 0; e < E; ++e) as[e] = 0.f;
+        constexpr int kU = 8;  // partials in flight
+        for (int c0 = 0; c0 < np; c0 += kU) {
+          float mc[kU], lc[kU], ac[kU][E];
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const bool in = c0 + u < nch;
-        const float* pc = part + (size_t)(c0 + u) * (D + 2);
-        mc[u] = in ? __ldcg(pc) : -INFINITY;
-        lc[u] = in ? __ldcg(pc + 1) : 0.f;
+          for (int x = 0; x < kU; ++x) {
+            const bool in = c0 + x < np;
+            const float* pc = partial(in ? c0 + x : 0, hh);
+            mc[x] = in ? __ldcg(pc) : -INFINITY;
+            lc[x] = in ? __ldcg(pc + 1) : 0.f;
 #pragma unroll
-        for (int e = 0; e < E; ++e) ac[u][e] = in ? __ldcg(pc + 2 + lane + 32 * e) : 0.f;
+            for (int e = 0; e < E; ++e) ac[x][e] = in ? __ldcg(pc + 2 + lane + 32 * e) : 0.f;
+          }
+          float nm = mx;
+#pragma unroll
+          for (int x = 0; x < kU; ++x) nm = fmaxf(nm, mc[x]);
+          const float corr = exp2_approx(mx - nm);  // 0 for the first partials
+          ls *= corr;
+#pragma unroll
+          for (int e = 0; e < E; ++e) as[e] *= corr;
+#pragma unroll
+          for (int x = 0; x < kU; ++x) {
+            const float f = exp2_approx(mc[x] - nm);  // 0 past the last partial
+            ls = fmaf(lc[x], f, ls);
+#pragma unroll
+            for (int e = 0; e < E; ++e) as[e] = fmaf(ac[x][e], f, as[e]);
+          }
+          mx = nm;
+        }
+        T* out = static_cast<T*>(p.out_t) + (head0 + hh) * D;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const float a_mem = den != 0.f ? num[e] / den : 0.f;
+          out[lane + 32 * e] = from_f32<T>(gm * a_mem + (1.f - gm) * (as[e] / ls));
+        }
       }
-      float nm = mx;
-#pragma unroll
-      for (int u = 0; u < kU; ++u) nm = fmaxf(nm, mc[u]);
-      const float corr = exp2_approx(mx - nm);  // 0 for the first partials
-      ls *= corr;
-#pragma unroll
-      for (int e = 0; e < E; ++e) as[e] *= corr;
-#pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const float f = exp2_approx(mc[u] - nm);  // 0 past the last partial
-        ls = fmaf(lc[u], f, ls);
-#pragma unroll
-        for (int e = 0; e < E; ++e) as[e] = fmaf(ac[u][e], f, as[e]);
-      }
-      mx = nm;
+      if (threadIdx.x == 0) *ctr = 0u;  // ready for the next step
     }
-    T* out = static_cast<T*>(p.out_t) + (head0 + hh) * D;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const float a_mem = den != 0.f ? num[e] / den : 0.f;
-      out[lane + 32 * e] = from_f32<T>(gm * a_mem + (1.f - gm) * (as[e] / ls));
+    u = e_unit;
+    if (attend && u < u_end) {
+      __syncthreads();  // `last` and the sums have been read
+      while (u >= off + segs * stream_units(p, b)) off += segs * stream_units(p, b++);
     }
   }
-  if (threadIdx.x == 0) *ctr = 0u;  // ready for the next step
 }
 
 // Rows of k and v [B, H_kv, n, D] into the buffers from row pos[b] on.  A
@@ -779,18 +956,40 @@ __global__ void __launch_bounds__(kThreads) q4_read_kernel(Q4Problem p, int n, T
   store8((key ? k : v) + ((size_t)bh * n + t) * D + 8 * w, out);
 }
 
+int chunks_of(int g) { return (g + kHeads - 1) / kHeads; }
+
+// Rows of a unit, and CTAs that attend.  A buffer whose full segments have at
+// most 4 units of 64 rows for each CTA that the GPU holds is cut into longer
+// units, one per CTA, none across a segment's end; with more work the units are
+// 64 rows and every CTA takes an equal run of them.
+struct Q4Plan {
+  int unit;
+  long long ctas, segments;
+};
+Q4Plan q4_plan(int B, int H_q, int H_kv, int S) {
+  const long long segments = (long long)B * H_kv * chunks_of(H_q / H_kv), most = kSMs * kResident;
+  const long long units = segments * ((S + kUnit - 1) / kUnit);
+  if (units > 4 * most) return {kUnit, most, segments};
+  const int per = (int)((units + most - 1) / most);
+  return {per * kUnit, segments * ((S + per * kUnit - 1) / (per * kUnit)), segments};
+}
+
 template <typename T, int D>
 cudaError_t launch(const Q4Problem& p, Q4What what, int n, void* k, void* v, cudaStream_t st) {
   const dim3 rows((unsigned)(((long long)n * (D / 8) + kThreads - 1) / kThreads), p.B * p.H_kv, 2);
   switch (what) {
     case Q4What::kStep: {
-      const int g = p.H_q / p.H_kv;
       constexpr int ring = kWarps * Ring<D>::kStages * Ring<D>::kSlot, sums = kWarps * kHeads * (D + 2) * 4;
       constexpr int bytes = ring > sums ? ring : sums;
-      cudaError_t e = cudaFuncSetAttribute(q4_decode_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-      if (e != cudaSuccess) return e;
+#ifdef QS
+      if (bytes > 48 * 1024) cudaFuncSetAttribute(q4_decode_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+#endif
+      const Q4Plan plan = q4_plan(p.B, p.H_q, p.H_kv, p.S);
+      Q4Problem q = p;
+      q.ctas = plan.ctas;
+      q.unit = plan.unit;
       q4_decode_kernel<T, D>
-          <<<dim3(p.nsplit + 1, p.B * p.H_kv, (g + kHeads - 1) / kHeads), kThreads, bytes, st>>>(p);
+          <<<(unsigned)(plan.ctas + plan.segments), kThreads, bytes, st>>>(q);
       break;
     }
     case Q4What::kAppend: q4_append_kernel<T, D><<<rows, kThreads, 0, st>>>(p, n); break;
@@ -813,15 +1012,11 @@ cudaError_t launch_type(const Q4Problem& p, Q4What what, int n, void* k, void* v
 
 }  // namespace
 
-int q4_head_chunks(int g) { return (g + kHeads - 1) / kHeads; }
+int q4_head_chunks(int g) { return chunks_of(g); }
 
-// Rows per CTA: one unit of 128 while that fills the GPU, then as many as
-// leave about four waves of resident CTAs (two per SM), at most 16 units.
-int q4_chunk_rows(long long groups, int S) {
-  const long long units = groups * ((S + kUnit - 1) / kUnit);
-  long long n = units / (kSMs * QB * QW);
-  n = n < 1 ? 1 : n > 16 ? 16 : n;
-  return (int)n * kUnit;
+// Partials: one per query head, and two sets of kHeads per CTA.
+size_t q4_partials(int B, int H_q, int H_kv, int S) {
+  return (size_t)B * H_q + (size_t)q4_plan(B, H_q, H_kv, S).ctas * 2 * kHeads;
 }
 
 cudaError_t launch_q4(const Q4Problem& p, Q4What what, int n, void* k, void* v, cudaStream_t st) {
