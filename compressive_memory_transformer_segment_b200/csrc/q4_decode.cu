@@ -44,7 +44,7 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kHeads = 8;               // query heads of a CTA (columns of a product)
-constexpr int kUnit = kWarps * 16;      // rows a CTA takes at a time
+constexpr int kUnit = kWarps * 32;      // rows of the smallest share of the work
 constexpr int kSMs = 148;
 #ifndef QB
 #define QB 3
@@ -189,45 +189,50 @@ template <typename T> struct Parts;
 template <> struct Parts<__nv_bfloat16> { static constexpr int n = 1; };
 template <> struct Parts<float> { static constexpr int n = 2; };
 
-// One warp's 16 rows, as a lane needs them: keys of rows k_row(i), + 8 (chunk
-// c), values of rows c, 4 + (c ^ 1), + 8, + 8 (chunk i), and the parameters of
-// rows k_row(i), + 8.  The product's index along the rows (i, or 2c and 2c + 1)
-// stands for row k_row(index) of its eight: an order in which the key loads
-// have no bank conflict and the value loads two-way ones.
+// The index of a product along 16 rows (i and i + 8, or 2c, 2c + 1, 2c + 8, 2c +
+// 9) stands for row k_row(index) of its eight: an order in which the key loads
+// from shared memory have no bank conflict and the value loads two-way ones.
 __device__ __forceinline__ int k_row(int i) { return (i & 1) ? 4 + ((i >> 1) ^ 1) : i >> 1; }
 
+// 16 rows as a lane needs them.  Keys: chunk c of rows k_row(i), + 8, their
+// parameters, and their minima (scales) in two groups as A fragments: groups
+// 2 (c & 1) and the next for d = 128, 0 and 1 for 64, 0 and 0 for 32.
 template <int D>
-struct Tile {
-  Raw<D / 8> k[2];
-  Raw<D / 8> kp[2], vp[2];
-  Raw<D / 16> v[4];
-  // Minima (scales) of rows k_row(i), + 8 in two groups, as A fragments: groups
-  // 2 (c & 1) and the next for d = 128, 0 and 1 for 64, 0 and 0 for 32.
+struct KeyTile {
+  Raw<D / 8> k[2], kp[2];
   uint32_t kmin[2], kcen[2];
 };
-
-// A warp's ring of tiles in shared memory, filled by asynchronous copies: the
-// loads of the next kStages - 1 tiles are in flight while one is used, without
-// registers to hold them.
+// Values: chunk i of rows k_row(2c), k_row(2c + 1), + 8, + 8; parameters of rows
+// k_row(i), + 8.
 template <int D>
+struct ValueTile {
+  Raw<D / 8> vp[2];
+  Raw<D / 16> v[4];
+};
+
+// A warp's ring in shared memory, filled by asynchronous copies of 16 TILES rows
+// at a time: the next slots' loads are in flight while one is used, without
+// registers to hold them.
+template <int D, int TILES>
 struct Ring {
-  static constexpr int kCodes = 16 * (D / 2), kParams = 16 * (D / 8);  // bytes of 16 rows
+  static constexpr int kRows = 16 * TILES;
+  static constexpr int kCodes = kRows * (D / 2), kParams = kRows * (D / 8);  // bytes of a slot's rows
   static constexpr int kSlot = 2 * kCodes + 2 * kParams;
-    #ifdef QS
+#ifdef QS
   static constexpr int kStages = QS;
 #else
-  static constexpr int kStages = 4;
+  static constexpr int kStages = TILES == 1 ? 4 : 2;
 #endif
   uint8_t* smem;
-  const uint8_t *k, *v, *par;  // this lane's source in the chunk's first 16 rows
-  int n, lane;                 // rows of the chunk
+  const uint8_t *k, *v, *kp, *vp;  // the first row
+  int n, lane;                     // rows
 
   __device__ __forceinline__ Ring(const Q4Problem& p, uint8_t* ring, size_t row0, int rows, int lane_)
       : smem(ring), n(rows), lane(lane_) {
-    const int chunk = D == 32 ? lane & 15 : lane;  // 16-byte pieces: D / 32 per row
-    k = p.k_codes + row0 * (D / 2) + chunk * 16;
-    v = p.v_codes + row0 * (D / 2) + chunk * 16;
-    par = reinterpret_cast<const uint8_t*>(lane < 16 ? p.k_scale : p.v_scale) + (row0 + (lane & 15)) * (D / 8);
+    k = p.k_codes + row0 * (D / 2);
+    v = p.v_codes + row0 * (D / 2);
+    kp = reinterpret_cast<const uint8_t*>(p.k_scale) + row0 * (D / 8);
+    vp = reinterpret_cast<const uint8_t*>(p.v_scale) + row0 * (D / 8);
   }
   template <int BYTES>
   __device__ __forceinline__ static void copy(uint32_t to, const uint8_t* src) {
@@ -242,33 +247,33 @@ struct Ring {
 #pragma unroll
     for (int e = 0; e < BYTES; e += 4) asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + e), "r"(0) : "memory");
   }
-  template <int BYTES, bool FULL>
-  __device__ __forceinline__ static void piece(uint32_t to, const uint8_t* src, bool in) {
-    if (FULL || in) copy<BYTES>(to, src);
-    else zero<BYTES>(to);
+  // Two arrays a and b of kRows rows of ROW bytes each, in pieces of BYTES, to
+  // `to` and behind one another; lanes take neighbouring pieces.
+  template <int ROW, int BYTES, bool FULL>
+  __device__ __forceinline__ void rows(uint32_t to, const uint8_t* a, const uint8_t* b, int left) const {
+    constexpr int kPieces = kRows * ROW / BYTES;  // of one array
+    static_assert(2 * kPieces % 32 == 0 && (kPieces % 32 == 0 || kPieces == 16), "whole turns of the warp");
+#pragma unroll
+    for (int e = 0; e < 2 * kPieces / 32; ++e) {
+      int piece = lane + 32 * (kPieces >= 32 ? e % (kPieces / 32 ? kPieces / 32 : 1) : 0);
+      const uint8_t* src = kPieces >= 32 ? (e < kPieces / 32 ? a : b) : (lane < 16 ? a : b);
+      if (kPieces < 32) piece &= 15;
+      const uint32_t dst = to + (lane + 32 * e) * BYTES;
+      if (FULL || piece * BYTES / ROW < left) copy<BYTES>(dst, src + piece * BYTES);
+      else zero<BYTES>(dst);
+    }
   }
   template <bool FULL>
   __device__ __forceinline__ void fill_rows(int slot, int r) const {
-    const uint32_t s = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + slot * kSlot + lane * 16;
-    const size_t off = (size_t)r * (D / 2);
-    if constexpr (D == 32) {
-      piece<16, FULL>(s, (lane < 16 ? k : v) + off, r + (lane & 15) < n);
-    } else {
-      constexpr int PR = D / 32;  // pieces per row
-      const uint8_t *ks = k + off, *vs = v + off;
-#pragma unroll
-      for (int e = 0; e < kCodes / 512; ++e) {
-        const bool in = r + (lane + 32 * e) / PR < n;
-        piece<16, FULL>(s + 512 * e, ks + 512 * e, in);
-        piece<16, FULL>(s + kCodes + 512 * e, vs + 512 * e, in);
-      }
-    }
-    piece<D / 8, FULL>(s + 2 * kCodes - lane * (16 - D / 8), par + (size_t)r * (D / 8), r + (lane & 15) < n);
+    const uint32_t s = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + slot * kSlot;
+    const size_t code = (size_t)r * (D / 2), par = (size_t)r * (D / 8);
+    rows<D / 2, 16, FULL>(s, k + code, v + code, n - r);
+    rows<D / 8, D / 8, FULL>(s + 2 * kCodes, kp + par, vp + par, n - r);
   }
-  // Starts the copy of rows r .. r + 15; rows from n on become zeros, whatever
-  // the buffer holds there.
+  // Starts the copy of rows r .. r + kRows - 1; rows from n on become zeros,
+  // whatever the buffer holds there.
   __device__ __forceinline__ void fill(int slot, int r) const {
-    if (r + 16 <= n) fill_rows<true>(slot, r);
+    if (r + kRows <= n) fill_rows<true>(slot, r);
     else fill_rows<false>(slot, r);
   }
   __device__ __forceinline__ static void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -276,23 +281,32 @@ struct Ring {
   __device__ __forceinline__ static void wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
   }
-  __device__ __forceinline__ void read(Tile<D>& t, int slot) const {
+  __device__ __forceinline__ void read(KeyTile<D>& t, int slot, int tile) const {
+    const int i = lane >> 2, c = lane & 3, kr = k_row(i) + 16 * tile;
     const uint8_t* s = smem + slot * kSlot;
-    const int i = lane >> 2, c = lane & 3, kr = k_row(i);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
+      const uint8_t* par = s + 2 * kCodes + (kr + 8 * e) * (D / 8);
       t.k[e].load(s + (kr + 8 * e) * (D / 2) + c * (D / 8));
-      t.kp[e].load(s + 2 * kCodes + (kr + 8 * e) * (D / 8));
-      t.vp[e].load(s + 2 * kCodes + kParams + (kr + 8 * e) * (D / 8));
+      t.kp[e].load(par);
       uint32_t a = t.kp[e].word(0), b = t.kp[e].word(D / 32 > 1 ? 1 : 0);
       if constexpr (D == 128) {
-        const uint2 w = *reinterpret_cast<const uint2*>(s + 2 * kCodes + (kr + 8 * e) * 16 + (c & 1) * 8);
+        const uint2 w = *reinterpret_cast<const uint2*>(par + (c & 1) * 8);
         a = w.x; b = w.y;
       }
       t.kmin[e] = __byte_perm(a, b, 0x7632);
       t.kcen[e] = __byte_perm(a, b, 0x5410);
-      t.v[2 * e].load(s + kCodes + (c + 8 * e) * (D / 2) + i * (D / 16));
-      t.v[2 * e + 1].load(s + kCodes + (4 + (c ^ 1) + 8 * e) * (D / 2) + i * (D / 16));
+    }
+  }
+  __device__ __forceinline__ void read(ValueTile<D>& t, int slot, int tile) const {
+    const int i = lane >> 2, c = lane & 3, kr = k_row(i) + 16 * tile;
+    const uint8_t* s = smem + slot * kSlot;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = 16 * tile + 8 * e;
+      t.vp[e].load(s + 2 * kCodes + kParams + (kr + 8 * e) * (D / 8));
+      t.v[2 * e].load(s + kCodes + (c + r) * (D / 2) + i * (D / 16));
+      t.v[2 * e + 1].load(s + kCodes + (4 + (c ^ 1) + r) * (D / 2) + i * (D / 16));
     }
   }
 };
@@ -362,7 +376,7 @@ __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) <
 // one part, 2^-12 of a term; fp32 heads: two, 2^-23), kept in its range by
 // powers of two: a head's query by its largest element, the probabilities
 // times scale by the largest scale seen.
-template <int D, int NP>
+template <int D, int NP, int TILES>
 struct Attention {
   static constexpr int NJ = D / 32;
   static constexpr bool kExact = NP > 1;
@@ -456,10 +470,10 @@ struct Attention {
   }
 
   // The reference becomes the maximum so far.
-  __device__ __forceinline__ void rebase(const float (&x)[4]) {
+  __device__ __forceinline__ void rebase(float top0, float top1) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const float mn = fmaxf(m[h], column_max(fmaxf(x[h], x[2 + h])));
+      const float mn = fmaxf(m[h], column_max(h ? top1 : top0));
       const float corr = exp2_approx(m[h] - mn);  // 0 for the first rows
       m[h] = mn;
       l[h] *= corr;
@@ -488,11 +502,9 @@ struct Attention {
     limit = min(to + 8 + 127, 255) << 7;
   }
 
-  // FULL: all 16 rows count; else rows k_row(i) (in0) and + 8 (in1) of a lane do
-  // or do not.
-  template <bool FULL>
-  __device__ __forceinline__ void step(const Tile<D>& t, bool in0, bool in1) {
-    // Scores of rows i (s[0], s[1]) and i + 8 (s[2], s[3]).
+  // Scores (as powers of two) of rows k_row(i) (x[0], x[1]) and + 8 (x[2],
+  // x[3]) of a tile; minus infinity for rows from `left` on.
+  __device__ __forceinline__ void scores(const KeyTile<D>& t, int left, int kr, float (&x)[4]) const {
     // The minima's share first: (minima of a row) times (sums of the queries).
     float s[4] = {0.f, 0.f, 0.f, 0.f};
     mma_bf16(s, t.kmin[0], t.kmin[1], t.kmin[0], t.kmin[1], qs[0], qs[1]);
@@ -517,26 +529,12 @@ struct Attention {
         for (int h = 0; h < 2; ++h) s[2 * e + h] = fmaf(sc, d[2 * e + h], s[2 * e + h]);
       }
     }
-    // Powers of two relative to a reference m, at most 2^kLead of it: a maximum
-    // is taken over the warp only when a score leaves that room (and by the
-    // first rows), not for every tile.
-    float x[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = FULL || (e < 2 ? in0 : in1) ? s[e] * f1 * f2[e & 1] : -INFINITY;
-    uint32_t top = 0;
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) top = __vimax3_u16x2(top, t.vp[0].word(j), t.vp[1].word(j));
-    top &= 0xffffu;  // the scales are the low halves
-    const float over = fmaxf(fmaxf(x[0], x[2]) - m[0], fmaxf(x[1], x[3]) - m[1]);
-    if (__any_sync(0xffffffffu, over > kLead || top > limit)) {
-      rebase(x);
-      raise(top);
-    }
-    float pr[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) pr[e] = exp2_approx(x[e] - m[e & 1]);
-    l[0] += pr[0] + pr[2];
-    l[1] += pr[1] + pr[3];
+    for (int e = 0; e < 4; ++e) x[e] = kr + 8 * (e >> 1) < left ? s[e] * f1 * f2[e & 1] : -INFINITY;
+  }
+
+  // O^T += V^T P^T of a tile with probabilities pr.
+  __device__ __forceinline__ void values(const ValueTile<D>& t, const float (&pr)[4]) {
     const float p2 = pow2(-pe);
     float w[4];
 #pragma unroll
@@ -565,6 +563,49 @@ struct Attention {
         mma_f16(o[2 * j], lo[0], lo[1], hi[0], hi[1], b0, b1);
         mma_f16(o[2 * j + 1], lo[2], lo[3], hi[2], hi[3], b0, b1);
       }
+    }
+  }
+
+  // A slot of the ring, of whose rows `left` count.
+  __device__ __forceinline__ void step(const Ring<D, TILES>& ring, int slot, int left) {
+    const int kr = k_row(ring.lane >> 2);
+    float x[TILES][4];
+#pragma unroll
+    for (int t = 0; t < TILES; ++t) {
+      KeyTile<D> keys;
+      ring.read(keys, slot, t);
+      scores(keys, left - 16 * t, kr, x[t]);
+    }
+    ValueTile<D> val[TILES];
+    uint32_t top = 0;
+#pragma unroll
+    for (int t = 0; t < TILES; ++t) {
+      ring.read(val[t], slot, t);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) top = __vimax3_u16x2(top, val[t].vp[0].word(j), val[t].vp[1].word(j));
+    }
+    top &= 0xffffu;  // the scales are the low halves
+    // Probabilities are powers of two relative to a reference m, at most
+    // 2^kLead: a maximum is taken over the warp only when a score leaves that
+    // room (and by the first rows), not every time.
+    float top0 = fmaxf(x[0][0], x[0][2]), top1 = fmaxf(x[0][1], x[0][3]);
+#pragma unroll
+    for (int t = 1; t < TILES; ++t) {
+      top0 = fmaxf(top0, fmaxf(x[t][0], x[t][2]));
+      top1 = fmaxf(top1, fmaxf(x[t][1], x[t][3]));
+    }
+    if (__any_sync(0xffffffffu, fmaxf(top0 - m[0], top1 - m[1]) > kLead || top > limit)) {
+      rebase(top0, top1);
+      raise(top);
+    }
+#pragma unroll
+    for (int t = 0; t < TILES; ++t) {
+      float pr[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) pr[e] = exp2_approx(x[t][e] - m[e & 1]);
+      l[0] += pr[0] + pr[2];
+      l[1] += pr[1] + pr[3];
+      values(val[t], pr);
     }
   }
 };
@@ -636,7 +677,9 @@ __global__ void __launch_bounds__(kThreads, Parts<T>::n == 1 ? kResident : 2)
 q4_decode_kernel(Q4Problem p) {
   constexpr int E = D / 32;  // channels per lane in the merges
   constexpr int NP = Parts<T>::n;
-  using R = Ring<D>;
+  constexpr int kTiles = NP == 1 ? 2 : 1;  // fp32 heads have no registers for two
+  using R = Ring<D, kTiles>;
+  constexpr int kTurn = kWarps * R::kRows;  // rows the CTA's warps take at a time
   extern __shared__ __align__(16) uint8_t smem[];
   float(*red)[kHeads][D + 2] = reinterpret_cast<float(*)[kHeads][D + 2]>(smem);  // [kWarps]
   __shared__ int last;
@@ -709,27 +752,21 @@ q4_decode_kernel(Q4Problem p) {
       R ring(p, smem + warp * R::kStages * R::kSlot, bh * p.S + r0, r1 - r0, lane);
 #pragma unroll
       for (int e = 0; e < R::kStages; ++e) {
-        const int r = warp * 16 + e * kUnit;
+        const int r = warp * R::kRows + e * kTurn;
         if (r < ring.n) ring.fill(e, r);
         ring.commit();
       }
-      Attention<D, NP> at;
+      Attention<D, NP, kTiles> at;
       at.init(q_t, ng, lane);
-      const int kr = k_row(i);
       int slot = 0;
-      for (int r = warp * 16; r < ring.n; r += kUnit) {
+      for (int r = warp * R::kRows; r < ring.n; r += kTurn) {
         ring.wait();
         __syncwarp();
-        Tile<D> t;
-        ring.read(t, slot);
+        at.step(ring, slot, ring.n - r);
         __syncwarp();  // every lane has read the slot
-        const int ahead = r + R::kStages * kUnit;
+        const int ahead = r + R::kStages * kTurn;
         if (ahead < ring.n) ring.fill(slot, ahead);
         ring.commit();
-        if (r + 16 <= ring.n)
-          at.template step<true>(t, true, true);
-        else
-          at.template step<false>(t, r + kr < ring.n, r + kr + 8 < ring.n);
         slot = slot + 1 < R::kStages ? slot + 1 : 0;
       }
       __syncthreads();  // the sums below lie where the rings were
@@ -959,9 +996,9 @@ __global__ void __launch_bounds__(kThreads) q4_read_kernel(Q4Problem p, int n, T
 int chunks_of(int g) { return (g + kHeads - 1) / kHeads; }
 
 // Rows of a unit, and CTAs that attend.  A buffer whose full segments have at
-// most 4 units of 64 rows for each CTA that the GPU holds is cut into longer
+// most 2 units of 128 rows for each CTA that the GPU holds is cut into longer
 // units, one per CTA, none across a segment's end; with more work the units are
-// 64 rows and every CTA takes an equal run of them.
+// 128 rows and every CTA takes an equal run of them.
 struct Q4Plan {
   int unit;
   long long ctas, segments;
@@ -969,7 +1006,7 @@ struct Q4Plan {
 Q4Plan q4_plan(int B, int H_q, int H_kv, int S) {
   const long long segments = (long long)B * H_kv * chunks_of(H_q / H_kv), most = kSMs * kResident;
   const long long units = segments * ((S + kUnit - 1) / kUnit);
-  if (units > 4 * most) return {kUnit, most, segments};
+  if (units > 2 * most) return {kUnit, most, segments};
   const int per = (int)((units + most - 1) / most);
   return {per * kUnit, segments * ((S + per * kUnit - 1) / (per * kUnit)), segments};
 }
@@ -979,7 +1016,8 @@ cudaError_t launch(const Q4Problem& p, Q4What what, int n, void* k, void* v, cud
   const dim3 rows((unsigned)(((long long)n * (D / 8) + kThreads - 1) / kThreads), p.B * p.H_kv, 2);
   switch (what) {
     case Q4What::kStep: {
-      constexpr int ring = kWarps * Ring<D>::kStages * Ring<D>::kSlot, sums = kWarps * kHeads * (D + 2) * 4;
+      using R = Ring<D, Parts<T>::n == 1 ? 2 : 1>;
+      constexpr int ring = kWarps * R::kStages * R::kSlot, sums = kWarps * kHeads * (D + 2) * 4;
       constexpr int bytes = ring > sums ? ring : sums;
 #ifdef QS
       if (bytes > 48 * 1024) cudaFuncSetAttribute(q4_decode_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
