@@ -1068,9 +1068,9 @@ Q4Problem q4_problem(const infini_dims_t* d, int seg_len, const CacheQ4& c) {
   return p;
 }
 
-// Workspace of a 4-bit decode step: [tickets | attention partials | retrieval].
+// Workspace of a 4-bit decode step: [tickets | partials].
 struct Q4Layout {
-  size_t part, ret, total;
+  size_t part, total;
 };
 
 int q4_layout(const infini_dims_t* d, int seg_len, Q4Layout* lay) {
@@ -1079,10 +1079,8 @@ int q4_layout(const infini_dims_t* d, int seg_len, Q4Layout* lay) {
   if (d->d_k != d->d_v || !head_dim_ok(d->d_k) || (long long)d->B * d->H_q > 65535 || seg_len > (1 << 30))
     return INFINI_ERR_UNSUPPORTED;
   const int zc = q4_head_chunks(d->H_q / d->H_kv);
-  const size_t BHq = (size_t)d->B * d->H_q, dd = d->d_k;
   lay->part = align_up((size_t)d->B * d->H_kv * zc * 4);
-  lay->ret = align_up(lay->part + q4_partials(d->B, d->H_q, d->H_kv, seg_len) * (dd + 2) * 4);
-  lay->total = align_up(lay->ret + BHq * (dd + 1) * 4);
+  lay->total = align_up(lay->part + q4_partial_bytes(d->B, d->H_q, d->H_kv, seg_len, d->d_k));
   return INFINI_OK;
 }
 
@@ -1241,7 +1239,6 @@ int infini_attn_decode_step_q4(const void* q_t, const void* k_t, const void* v_t
   p.q_t = q_t; p.k_t = k_t; p.v_t = v_t; p.beta = beta; p.pos = pos; p.M = M; p.z = z; p.out_t = out_t;
   p.ctr = reinterpret_cast<unsigned int*>(ws);
   p.part = reinterpret_cast<float*>(ws + lay.part);
-  p.ret = reinterpret_cast<float*>(ws + lay.ret);
   cudaError_t e = launch_q4(p, Q4What::kStep, 1, nullptr, nullptr, st);
   if (owned) {
     cudaError_t f = cudaFreeAsync(ws, st);

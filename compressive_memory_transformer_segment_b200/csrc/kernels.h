@@ -215,17 +215,16 @@ struct Q4Problem {
   const float* M;         // [B, H_kv, d, d]
   const float* z;         // [B, H_kv, d]
   void* out_t;            // [B, H_q, d]
-  float* part;            // workspace: [partials][d + 2]
-  float* ret;             // workspace: [B * H_q][d + 1]
+  float* part;            // workspace: partials (q4_partial_bytes)
   unsigned int* ctr;      // workspace: [B * H_kv][head chunks] tickets, 0 between steps
   int B, H_q, H_kv, d, S;
-  int unit, ctas;         // set by the launcher: rows of a unit, CTAs that attend
+  int unit, lead, ctas;   // set by the launcher: rows of a unit, units for a segment itself, CTAs
   bool bf16;
   unsigned int* status;
 };
 enum class Q4What { kStep, kAppend, kRead };
 int q4_head_chunks(int g);
-size_t q4_partials(int B, int H_q, int H_kv, int S);
+size_t q4_partial_bytes(int B, int H_q, int H_kv, int S, int d);
 cudaError_t launch_q4(const Q4Problem& p, Q4What what, int n, void* k, void* v, cudaStream_t stream);
 
 int decode_splits(int S);

@@ -28,8 +28,8 @@
 // Grid: the rows of all (stream, KV head, chunk of 8 query heads) are shared out
 // in equal parts over as many CTAs as the GPU holds, whatever the streams'
 // lengths (read from device memory: one captured launch serves every
-// position); one more CTA each reads the memory (sigma(q) M, sigma(q) z).  The
-// last of a head chunk's CTAs to finish (a ticket) merges their partials in
+// position), and the rows of the memory for sigma(q) M, sigma(q) z with them.
+// The last of a head chunk's CTAs to finish (a ticket) merges their partials in
 // order and writes the output.  No CTA waits for another.
 #include <cuda_fp16.h>
 
@@ -49,6 +49,10 @@ constexpr int kSMs = 148;
 #ifndef QB
 #define QB 3
 #endif
+#ifndef QL
+#define QL 4
+#endif
+constexpr int kLeadUnits = QL;
 constexpr int kResident = QB;  // CTAs per SM (bf16 heads; two for fp32 ones)
 
 template <int BYTES> struct RawBytes;
@@ -122,11 +126,29 @@ __device__ __forceinline__ void store_group(const float (&x)[8], int w, uint8_t*
   par.x = __float2bfloat16_rn(__fmul_rn(fmaxf(__fsub_rn(hi, m), 0.f), 1.f / 15.f));
   const float s = __bfloat162float(par.x);
   if (nan) par = __floats2bfloat162_rn(NAN, NAN);
+  // Codes: the rounded quotient (x - m) / s, to the nearest integer.  A product
+  // with the reciprocal decides it unless it lies within 2^-10 of a half, where
+  // the division itself does (rarely, so the eight divisions' code is one loop).
+  const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
   uint32_t q[8];
+  uint32_t close = 0;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const float t = s > 0.f ? rintf(__fdiv_rn(__fsub_rn(x[e], m), s)) : 0.f;
-    q[e] = (uint32_t)fminf(fmaxf(t, 0.f), 15.f);
+    const float t = __fsub_rn(x[e], m) * inv, n = rintf(t);
+    if (!(fabsf(t - n) < 0.499f) && inv > 0.f) close |= 1u << e;
+    q[e] = (uint32_t)fminf(fmaxf(n, 0.f), 15.f);
+  }
+  if (close) {
+#pragma unroll 1
+    for (int e = 0; e < 8; ++e) {
+      if (!(close >> e & 1)) continue;
+      float v = x[0];
+#pragma unroll
+      for (int k = 1; k < 8; ++k) v = k == e ? x[k] : v;
+      const float n = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(v, m), s)), 0.f), 15.f);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) q[k] = k == e ? (uint32_t)n : q[k];
+    }
   }
   if (!active) return;
   if constexpr (KEY) {
@@ -210,25 +232,25 @@ struct ValueTile {
   Raw<D / 16> v[4];
 };
 
-// A warp's ring in shared memory, filled by asynchronous copies of 16 TILES rows
-// at a time: the next slots' loads are in flight while one is used, without
-// registers to hold them.
-template <int D, int TILES>
+// A warp's ring in shared memory, filled by asynchronous copies of 16 rows at a
+// time: the next slots' loads are in flight while two are used (one's keys, the
+// one before's values), without registers to hold them.
+template <int D>
 struct Ring {
-  static constexpr int kRows = 16 * TILES;
+  static constexpr int kRows = 16;
   static constexpr int kCodes = kRows * (D / 2), kParams = kRows * (D / 8);  // bytes of a slot's rows
   static constexpr int kSlot = 2 * kCodes + 2 * kParams;
 #ifdef QS
   static constexpr int kStages = QS;
 #else
-  static constexpr int kStages = TILES == 1 ? 4 : 2;
+  static constexpr int kStages = 4;
 #endif
   uint8_t* smem;
   const uint8_t *k, *v, *kp, *vp;  // the first row
   int n, lane;                     // rows
 
-  __device__ __forceinline__ Ring(const Q4Problem& p, uint8_t* ring, size_t row0, int rows, int lane_)
-      : smem(ring), n(rows), lane(lane_) {
+  __device__ __forceinline__ void set(const Q4Problem& p, uint8_t* ring, size_t row0, int rows, int lane_) {
+    smem = ring; n = rows; lane = lane_;
     k = p.k_codes + row0 * (D / 2);
     v = p.v_codes + row0 * (D / 2);
     kp = reinterpret_cast<const uint8_t*>(p.k_scale) + row0 * (D / 8);
@@ -255,7 +277,7 @@ struct Ring {
     static_assert(2 * kPieces % 32 == 0 && (kPieces % 32 == 0 || kPieces == 16), "whole turns of the warp");
 #pragma unroll
     for (int e = 0; e < 2 * kPieces / 32; ++e) {
-      int piece = lane + 32 * (kPieces >= 32 ? e % (kPieces / 32 ? kPieces / 32 : 1) : 0);
+      int piece = lane + 32 * (kPieces >= 32 ? e % (kPieces >= 32 ? kPieces / 32 : 1) : 0);
       const uint8_t* src = kPieces >= 32 ? (e < kPieces / 32 ? a : b) : (lane < 16 ? a : b);
       if (kPieces < 32) piece &= 15;
       const uint32_t dst = to + (lane + 32 * e) * BYTES;
@@ -273,16 +295,18 @@ struct Ring {
   // Starts the copy of rows r .. r + kRows - 1; rows from n on become zeros,
   // whatever the buffer holds there.
   __device__ __forceinline__ void fill(int slot, int r) const {
-    if (r + kRows <= n) fill_rows<true>(slot, r);
+    if (__builtin_expect(r + kRows <= n, 1)) fill_rows<true>(slot, r);
     else fill_rows<false>(slot, r);
   }
   __device__ __forceinline__ static void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-  // Waits until at most kStages - 1 groups of this lane are in flight.
+  // Waits until at most LEFT groups of this lane are in flight.
+  template <int LEFT>
   __device__ __forceinline__ static void wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+    __syncwarp();
   }
-  __device__ __forceinline__ void read(KeyTile<D>& t, int slot, int tile) const {
-    const int i = lane >> 2, c = lane & 3, kr = k_row(i) + 16 * tile;
+  __device__ __forceinline__ void read(KeyTile<D>& t, int slot) const {
+    const int i = lane >> 2, c = lane & 3, kr = k_row(i);
     const uint8_t* s = smem + slot * kSlot;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -298,12 +322,27 @@ struct Ring {
       t.kcen[e] = __byte_perm(a, b, 0x5410);
     }
   }
-  __device__ __forceinline__ void read(ValueTile<D>& t, int slot, int tile) const {
-    const int i = lane >> 2, c = lane & 3, kr = k_row(i) + 16 * tile;
+  // The largest scale of the values of 32 / (D / 8) .. rows of this lane, as bf16
+  // bits: the lanes' share of a slot's 16 rows together.
+  __device__ __forceinline__ uint32_t top_scale(int slot) const {
+    const uint8_t* s = smem + slot * kSlot + 2 * kCodes + kParams;
+    Raw<D / 16> half;  // half a row's parameters per lane
+    uint32_t top = 0;
+    if constexpr (D == 32) {
+      top = *reinterpret_cast<const uint32_t*>(s + (lane & 15) * 4);
+    } else {
+      half.load(s + lane * (D / 16));
+#pragma unroll
+      for (int j = 0; j < D / 64; ++j) top = __vmaxu2(top, half.word(j));
+    }
+    return top & 0xffffu;  // the scales are the low halves
+  }
+  __device__ __forceinline__ void read(ValueTile<D>& t, int slot) const {
+    const int i = lane >> 2, c = lane & 3, kr = k_row(i);
     const uint8_t* s = smem + slot * kSlot;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int r = 16 * tile + 8 * e;
+      const int r = 8 * e;
       t.vp[e].load(s + 2 * kCodes + kParams + (kr + 8 * e) * (D / 8));
       t.v[2 * e].load(s + kCodes + (c + r) * (D / 2) + i * (D / 16));
       t.v[2 * e + 1].load(s + kCodes + (4 + (c ^ 1) + r) * (D / 2) + i * (D / 16));
@@ -376,7 +415,7 @@ __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) <
 // one part, 2^-12 of a term; fp32 heads: two, 2^-23), kept in its range by
 // powers of two: a head's query by its largest element, the probabilities
 // times scale by the largest scale seen.
-template <int D, int NP, int TILES>
+template <int D, int NP>
 struct Attention {
   static constexpr int NJ = D / 32;
   static constexpr bool kExact = NP > 1;
@@ -566,54 +605,67 @@ struct Attention {
     }
   }
 
-  // A slot of the ring, of whose rows `left` count.
-  __device__ __forceinline__ void step(const Ring<D, TILES>& ring, int slot, int left) {
-    const int kr = k_row(ring.lane >> 2);
-    float x[TILES][4];
-#pragma unroll
-    for (int t = 0; t < TILES; ++t) {
-      KeyTile<D> keys;
-      ring.read(keys, slot, t);
-      scores(keys, left - 16 * t, kr, x[t]);
-    }
-    ValueTile<D> val[TILES];
-    uint32_t top = 0;
-#pragma unroll
-    for (int t = 0; t < TILES; ++t) {
-      ring.read(val[t], slot, t);
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) top = __vimax3_u16x2(top, val[t].vp[0].word(j), val[t].vp[1].word(j));
-    }
-    top &= 0xffffu;  // the scales are the low halves
-    // Probabilities are powers of two relative to a reference m, at most
-    // 2^kLead: a maximum is taken over the warp only when a score leaves that
-    // room (and by the first rows), not every time.
-    float top0 = fmaxf(x[0][0], x[0][2]), top1 = fmaxf(x[0][1], x[0][3]);
-#pragma unroll
-    for (int t = 1; t < TILES; ++t) {
-      top0 = fmaxf(top0, fmaxf(x[t][0], x[t][2]));
-      top1 = fmaxf(top1, fmaxf(x[t][1], x[t][3]));
-    }
-    if (__any_sync(0xffffffffu, fmaxf(top0 - m[0], top1 - m[1]) > kLead || top > limit)) {
+  // Probabilities (powers of two relative to a reference m, at most 2^kLead) of
+  // a tile from its scores x; top: the largest scale of this lane's rows, as
+  // bf16 bits.  A maximum is taken over the warp only when a score leaves that
+  // room (and by the first rows), not for every tile.
+  __device__ __forceinline__ void probabilities(const float (&x)[4], uint32_t top, float (&pr)[4]) {
+    const float top0 = fmaxf(x[0], x[2]), top1 = fmaxf(x[1], x[3]);
+    if (__builtin_expect(__any_sync(0xffffffffu, fmaxf(top0 - m[0], top1 - m[1]) > kLead || top > limit), 0)) {
       rebase(top0, top1);
       raise(top);
     }
 #pragma unroll
-    for (int t = 0; t < TILES; ++t) {
-      float pr[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) pr[e] = exp2_approx(x[t][e] - m[e & 1]);
-      l[0] += pr[0] + pr[2];
-      l[1] += pr[1] + pr[3];
-      values(val[t], pr);
+    for (int e = 0; e < 4; ++e) pr[e] = exp2_approx(x[e] - m[e & 1]);
+    l[0] += pr[0] + pr[2];
+    l[1] += pr[1] + pr[3];
+  }
+
+  // All of a ring's rows of this warp (every kWarps-th 16).  A turn computes one
+  // tile's scores and the tile before's products with the values: two chains
+  // that do not wait for each other, in the code of one tile.
+  __device__ __forceinline__ void run(const Ring<D>& ring, int warp) {
+    using R = Ring<D>;
+    constexpr int kTurn = kWarps * R::kRows;
+    const int kr = k_row(ring.lane >> 2);
+    float pr[4] = {0.f, 0.f, 0.f, 0.f};
+    int slot = 0, before = R::kStages - 1;
+    for (int r = warp * R::kRows; r < ring.n; r += kTurn) {
+      // Of the kStages groups before this turn's the first is needed; the slot
+      // of two tiles ago is free, the one of the tile before is read below.
+      R::template wait<R::kStages - 2>();
+      KeyTile<D> keys;
+      ring.read(keys, slot);
+      float x[4];
+      scores(keys, ring.n - r, kr, x);
+      ValueTile<D> val;
+      if (r >= kTurn) {
+        ring.read(val, before);
+        values(val, pr);
+        __syncwarp();  // every lane has read the slot
+      }
+      const int ahead = r + (R::kStages - 1) * kTurn;
+      if (ahead < ring.n) ring.fill(before, ahead);
+      R::commit();
+      const uint32_t top = ring.top_scale(slot);
+      probabilities(x, top, pr);
+      before = slot;
+      slot = slot + 1 < R::kStages ? slot + 1 : 0;
     }
+    if (warp * R::kRows < ring.n) {
+      ValueTile<D> val;
+      ring.read(val, before);
+      values(val, pr);
+    }
+    __syncwarp();
   }
 };
 
-// Units of p.unit rows of stream b (0: idle).
+// Units of a segment of stream b (0: idle): p.lead for what a segment costs
+// whatever its length, then one for each p.unit rows.
 __device__ __forceinline__ uint32_t stream_units(const Q4Problem& p, int b) {
   const int pos = p.pos[b];
-  return pos >= 0 && pos < p.S ? pos / p.unit + 1 : 0;
+  return pos >= 0 && pos < p.S ? p.lead + pos / p.unit + 1 : 0;
 }
 
 // How the units of all segments are shared out.  A segment is what one (stream,
@@ -623,25 +675,33 @@ __device__ __forceinline__ uint32_t stream_units(const Q4Problem& p, int b) {
 // the streams' lengths are.  (A launch whose units are no more than its CTAs has
 // one unit per CTA: none then has two segments.)
 struct Share {
-  uint32_t units, ctas;
-  __device__ __forceinline__ uint32_t first(uint32_t k) const {
-    return (uint32_t)((unsigned long long)k * units / ctas);
+  uint32_t units, ctas, per, rest;  // units = ctas per + rest
+  __device__ __forceinline__ void set(uint32_t total, uint32_t most) {
+    units = total;
+    ctas = min(most, total);
+    per = ctas ? total / ctas : 0;
+    rest = total - per * ctas;
   }
+  // (rest is 0 or ctas at most a few hundred: the product fits.)
+  __device__ __forceinline__ uint32_t first(uint32_t k) const { return k * per + k * rest / ctas; }
   __device__ __forceinline__ uint32_t owner(uint32_t u) const {
-    return (uint32_t)(((unsigned long long)(u + 1) * ctas + units - 1) / units) - 1;
+    // Near enough that a turn or two set it right.
+    uint32_t k = min((uint32_t)((float)u * ((float)ctas / (float)units)), ctas - 1);
+    while (first(k) > u) --k;
+    while (first(k + 1) <= u) ++k;
+    return k;
   }
 };
 
-// Adds up the streams' units (the whole CTA calls it): the total, and the
-// stream and its first unit that `unit_of(total)` lies in, or, for by_stream,
-// of stream `unit_of(total)`.
-template <typename F>
-__device__ __forceinline__ uint32_t locate(const Q4Problem& p, uint32_t segs, bool by_stream, F&& unit_of,
-                                           uint32_t& stream, uint32_t& start) {
+// Adds up the streams' units (the whole CTA calls it), shares them out, and
+// finds the stream that this CTA's first unit lies in, and its first unit.
+__device__ __forceinline__ void locate(const Q4Problem& p, uint32_t segs, Share& share, uint32_t& stream,
+                                       uint32_t& start) {
   __shared__ uint32_t sums[kWarps], found[2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int per = (p.B + kThreads - 1) / kThreads, b0 = min((int)threadIdx.x * per, p.B), b1 = min(b0 + per, p.B);
   uint32_t mine = 0;
+#pragma unroll 1
   for (int b = b0; b < b1; ++b) mine += stream_units(p, b) * segs;
   uint32_t incl = mine;
 #pragma unroll
@@ -657,286 +717,336 @@ __device__ __forceinline__ uint32_t locate(const Q4Problem& p, uint32_t segs, bo
     if (w < warp) at += sums[w];
     total += sums[w];
   }
-  const uint32_t want = unit_of(total);
-  for (int b = b0; b < b1; ++b) {
-    const uint32_t n = stream_units(p, b) * segs;
-    if (by_stream ? b == (int)want : want >= at && want < at + n) {
-      found[0] = b;
-      found[1] = at;
+  share.set(total, p.ctas);
+  if (blockIdx.x >= share.ctas) return;
+  const uint32_t want = share.first(blockIdx.x);
+  if (want >= at && want < at + mine) {
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) {
+      const uint32_t n = stream_units(p, b) * segs;
+      if (want < at + n) {
+        found[0] = b;
+        found[1] = at;
+        break;
+      }
+      at += n;
     }
-    at += n;
   }
   __syncthreads();
   stream = found[0];
   start = found[1];
-  return total;
 }
+
+// A run of units of one segment, and the segment's place.
+struct Run {
+  uint32_t b, off, seg;  // stream, its first unit, segment of the stream
+  uint32_t s0, s1;       // the segment's units of rows
+  uint32_t u, end;       // the run's
+  int pos, hk, hq0, ng;  // token's row; KV head; query heads hq0 .. hq0 + ng - 1
+  __device__ __forceinline__ size_t bh(const Q4Problem& p) const { return (size_t)b * p.H_kv + hk; }
+  __device__ __forceinline__ size_t head0(const Q4Problem& p) const { return (size_t)b * p.H_q + hq0; }
+  __device__ __forceinline__ bool whole() const { return u == s0 && end == s1; }
+};
+
+// What a CTA leaves of a run, per head: the attention over its rows (max
+// reference m, sum l, acc[D]) and its share of the retrieval, sigma(q) M in
+// kThreads / D parts and sigma(q) z.
+template <int D>
+struct Partial {
+  float acc[D];
+  float num[kThreads];
+  float m, l, den, unused;
+};
+
+// The ticket of a segment, taken once a CTA's share of it is in the workspace;
+// the last CTA merges the partials in CTA order, with the gate.  The whole CTA
+// calls it; no CTA waits for another.
+template <typename T, int D>
+__device__ __forceinline__ void finish(const Q4Problem& p, const Share& share, const Run& r, uint32_t segs) {
+  constexpr int E = D / 32;  // channels per lane
+  __shared__ int last;       // partials to merge, 0 if this CTA is not the last
+  __shared__ uint32_t first_cta;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  unsigned int* ctr = p.ctr + (size_t)r.b * segs + r.seg;
+  Partial<D>* part = reinterpret_cast<Partial<D>*>(p.part);
+  __syncthreads();  // every thread's share is written
+  if (threadIdx.x == 0) {
+    const uint32_t k0 = r.whole() ? blockIdx.x : share.owner(r.s0);
+    const uint32_t n = r.whole() ? 1 : share.owner(r.s1 - 1) - k0 + 1;
+    __threadfence();  // (cumulative: the barrier put the CTA's writes before it)
+    last = n == 1 || atomicAdd(ctr, 1u) == n - 1 ? (int)n : 0;
+    first_cta = k0;
+    __threadfence();  // every other CTA's writes are visible
+  }
+  __syncthreads();
+  const int np = last;
+  if (np == 0) return;
+  const size_t head0 = r.head0(p);
+  // Partial x of head hh: a CTA that has the segment whole leaves it at the
+  // heads' own place; of several the first may have had another before this one.
+  const bool later = np > 1 && share.first(first_cta) < r.s0 - p.lead;
+  const Partial<D>* mine = part + (np == 1 ? head0 : (size_t)p.B * p.H_q + (size_t)first_cta * 2 * kHeads);
+  for (int hh = warp; hh < r.ng; hh += kWarps) {
+    auto at = [&](int x) { return mine + (size_t)x * 2 * kHeads + (x == 0 && later ? kHeads : 0) + hh; };
+    float mx = -INFINITY;
+#pragma unroll 1
+    for (int x = lane; x < np; x += 32) mx = fmaxf(mx, __ldcg(&at(x)->m));
+    mx = warp_max(mx);
+    float ls = 0.f, den = 0.f, as[E], num[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) as[e] = num[e] = 0.f;
+#pragma unroll 1
+    for (int x0 = 0; x0 < np; x0 += 32) {
+      float w = 0.f, lx = 0.f, dx = 0.f;
+      if (x0 + lane < np) {
+        const Partial<D>* q = at(x0 + lane);
+        w = exp2_approx(__ldcg(&q->m) - mx);
+        lx = __ldcg(&q->l) * w;
+        dx = __ldcg(&q->den);
+      }
+      ls += warp_sum(lx);
+      den += warp_sum(dx);
+      const int n = min(32, np - x0);
+#pragma unroll 4
+      for (int k = 0; k < n; ++k) {
+        const Partial<D>* q = at(x0 + k);
+        const float wk = __shfl_sync(0xffffffffu, w, k);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          as[e] = fmaf(__ldcg(&q->acc[lane + 32 * e]), wk, as[e]);
+#pragma unroll
+          for (int u = 0; u < kThreads / D; ++u) num[e] += __ldcg(&q->num[u * D + lane + 32 * e]);
+        }
+      }
+    }
+    const float gm = gate_sigmoid(p.beta[r.hq0 + hh]);
+    T* out = static_cast<T*>(p.out_t) + (head0 + hh) * D;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const float a_mem = den != 0.f ? num[e] / den : 0.f;
+      out[lane + 32 * e] = from_f32<T>(gm * a_mem + (1.f - gm) * (as[e] / ls));
+    }
+  }
+  if (threadIdx.x == 0) *ctr = 0u;  // ready for the next step
+}
+
+// A CTA's share of the retrieval: sigma(q) M and sigma(q) z over M's rows [k0,
+// k1), which the CTAs of a segment split as they split its rows.  The first 32
+// of them are copied to shared memory while the rows are attended to.
+template <int D>
+struct Retrieval {
+  static constexpr int kRows = 32;
+  static constexpr int kBytes = (kRows * D + D * kHeads) * 4;
+  float* buf;             // [kRows][D]
+  float (*sq)[kHeads];    // [D]: sigma(q), k0's first
+  int k0, k1;
+  const float* M;
+  float den;              // sigma(q) z of this thread's head
+  __device__ __forceinline__ void copy(int k) const {
+    const int n = min(kRows, k1 - k) * D / 4;  // 16-byte pieces
+#pragma unroll 2
+    for (int x = threadIdx.x; x < n; x += kThreads) {
+      const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(buf + 4 * x));
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(M + (size_t)k * D + 4 * x) : "memory");
+    }
+  }
+  template <typename T>
+  __device__ __forceinline__ void begin(const Q4Problem& p, const Run& r, uint8_t* smem) {
+    buf = reinterpret_cast<float*>(smem);
+    sq = reinterpret_cast<float(*)[kHeads]>(buf + kRows * D);
+    // By units: the runs of a segment tile its rows, and M's with them.
+    const uint32_t n = r.s1 - r.s0;
+    k0 = (int)((unsigned long long)(r.u - r.s0) * D / n);
+    k1 = (int)((unsigned long long)(r.end - r.s0) * D / n);
+    M = p.M + r.bh(p) * D * D;
+    copy(k0);
+    // sigma(q) and its product with z: 16 threads a head, all loads first.
+    const int hh = threadIdx.x / 16, t = threadIdx.x % 16;
+    const T* q = static_cast<const T*>(p.q_t) + (r.head0(p) + (hh < r.ng ? hh : 0)) * D + k0;
+    const float* z = p.z + r.bh(p) * D + k0;
+    float qv[D / 16], zv[D / 16];
+#pragma unroll
+    for (int e = 0; e < D / 16; ++e) {
+      const bool in = t + 16 * e < k1 - k0;
+      qv[e] = in ? to_f32<T>(q[t + 16 * e]) : 0.f;
+      zv[e] = in ? z[t + 16 * e] : 0.f;
+    }
+    den = 0.f;
+#pragma unroll
+    for (int e = 0; e < D / 16; ++e) {
+      const float s = elu1(qv[e]);
+      if (t + 16 * e < k1 - k0) sq[t + 16 * e][hh] = s;
+      den = fmaf(s, zv[e], den);
+    }
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+  }
+  // After the copies of begin() are waited for and a barrier.
+  __device__ __forceinline__ void end(Partial<D>* part, int ng) const {
+    const int col = threadIdx.x % D, u = threadIdx.x / D;  // this thread's column and part
+    float acc[kHeads];
+#pragma unroll
+    for (int hh = 0; hh < kHeads; ++hh) acc[hh] = 0.f;
+    auto add = [&](int row, float mv) {  // row: relative to k0
+      const float4 lo = *reinterpret_cast<const float4*>(sq[row]);
+      const float4 hi = *reinterpret_cast<const float4*>(sq[row] + 4);
+      acc[0] = fmaf(lo.x, mv, acc[0]); acc[1] = fmaf(lo.y, mv, acc[1]);
+      acc[2] = fmaf(lo.z, mv, acc[2]); acc[3] = fmaf(lo.w, mv, acc[3]);
+      acc[4] = fmaf(hi.x, mv, acc[4]); acc[5] = fmaf(hi.y, mv, acc[5]);
+      acc[6] = fmaf(hi.z, mv, acc[6]); acc[7] = fmaf(hi.w, mv, acc[7]);
+    };
+    constexpr int kStep = kThreads / D, kB = 8;  // rows in flight behind the first 32
+    const int n = min(kRows, k1 - k0);
+#pragma unroll 4
+    for (int x = u; x < n; x += kStep) add(x, buf[x * D + col]);
+#pragma unroll 1
+    for (int x0 = kRows + u; x0 < k1 - k0; x0 += kB * kStep) {
+      float mv[kB];
+#pragma unroll
+      for (int e = 0; e < kB; ++e) {
+        const int x = x0 + e * kStep;
+        mv[e] = x < k1 - k0 ? __ldcs(M + (size_t)(k0 + x) * D + col) : 0.f;
+      }
+#pragma unroll
+      for (int e = 0; e < kB; ++e)
+        if (x0 + e * kStep < k1 - k0) add(x0 + e * kStep, mv[e]);
+    }
+#pragma unroll
+    for (int hh = 0; hh < kHeads; ++hh)
+      if (hh < ng) part[hh].num[threadIdx.x] = acc[hh];
+    if (threadIdx.x % 16 == 0 && (int)threadIdx.x / 16 < ng) part[threadIdx.x / 16].den = den;
+  }
+};
+
+template <int D> constexpr int kRingBytes = kWarps * Ring<D>::kStages * Ring<D>::kSlot;
+template <int D> constexpr int kSumBytes = kWarps * kHeads * (D + 2) * 4;
+// The sums lie where the retrieval's rows were.
+template <int D>
+constexpr int kSmemBytes = kRingBytes<D> + (kSumBytes<D> > Retrieval<D>::kBytes ? kSumBytes<D> : Retrieval<D>::kBytes);
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, Parts<T>::n == 1 ? kResident : 2)
 q4_decode_kernel(Q4Problem p) {
-  constexpr int E = D / 32;  // channels per lane in the merges
+  static_assert(kThreads == 16 * kHeads, "16 threads a head");
   constexpr int NP = Parts<T>::n;
-  constexpr int kTiles = NP == 1 ? 2 : 1;  // fp32 heads have no registers for two
-  using R = Ring<D, kTiles>;
+  using R = Ring<D>;
   constexpr int kTurn = kWarps * R::kRows;  // rows the CTA's warps take at a time
   extern __shared__ __align__(16) uint8_t smem[];
-  float(*red)[kHeads][D + 2] = reinterpret_cast<float(*)[kHeads][D + 2]>(smem);  // [kWarps]
-  __shared__ int last;
+  float(*red)[kHeads][D + 2] = reinterpret_cast<float(*)[kHeads][D + 2]>(smem + kRingBytes<D>);  // [kWarps]
 
   const int g = p.H_q / p.H_kv, zc = (g + kHeads - 1) / kHeads;
   const uint32_t segs = (uint32_t)(p.H_kv * zc);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int i = lane >> 2, c = lane & 3;
-  // The retrievals come first: they are short and every output waits for one.
-  const uint32_t retrievals = (uint32_t)p.B * segs;
-  const bool attend = blockIdx.x >= retrievals;
-  const uint32_t cta = blockIdx.x - retrievals;
-
-  uint32_t b, off;  // stream, its first unit
-  Share share;
-  uint32_t u, u_end, seg;  // units of this CTA; segment of the stream
-  if (attend) {
-    share.units = locate(p, segs, false, [&](uint32_t total) {
-      share = {total, min((uint32_t)p.ctas, total)};
-      return cta < share.ctas ? share.first(cta) : 0u;
-    }, b, off);
-    if (cta >= share.ctas) return;
-    u = share.first(cta);
-    u_end = share.first(cta + 1);
-  } else {
-    const uint32_t stream = blockIdx.x / segs;
-    seg = blockIdx.x - stream * segs;
-    share.units = locate(p, segs, true, [&](uint32_t) { return stream; }, b, off);
-    share.ctas = min((uint32_t)p.ctas, share.units);
-    const int pos = p.pos[b];
-    if (pos < 0 || pos >= p.S) {  // an idle stream; nothing of it is touched
-      if (pos != -1 && seg == 0 && threadIdx.x == 0) atomicOr(p.status, kStatusRange);
-      return;
-    }
-    u = off;
-    u_end = off + 1;  // one turn of the loop
+  if (blockIdx.x == 0) {
+    // A position that is neither a row nor -1: reported, the stream left alone.
+#pragma unroll 1
+    for (int b = threadIdx.x; b < p.B; b += kThreads)
+      if (p.pos[b] < -1 || p.pos[b] >= p.S) atomicOr(p.status, kStatusRange);
   }
-
-  for (bool first = true; u < u_end; first = false) {
-    const int pos = p.pos[b];
-    const uint32_t n = pos / p.unit + 1;
-    if (attend) seg = (u - off) / n;
-    const uint32_t s0 = off + seg * n, s1 = s0 + n;  // the segment's units
-    const uint32_t e_unit = attend ? min(u_end, s1) : u_end;
-    const int hk = seg / zc, hq0 = hk * g + (seg - hk * zc) * kHeads;
-    const int ng = min(kHeads, (hk + 1) * g - hq0);
-    const size_t bh = (size_t)b * p.H_kv + hk;
-    const size_t head0 = (size_t)b * p.H_q + hq0;
-    const T* q_t = static_cast<const T*>(p.q_t) + head0 * D;
-    // Partials of a segment: of a CTA that has it whole, at the segment's own
-    // place; of others, at the CTA's (its first segment, or its last).
-    const uint32_t k_first = share.owner(s0), k_last = share.owner(s1 - 1);
-
-    if (attend) {
-      // ---------------------------------------------- attention partial
-      const int r0 = (u - s0) * p.unit;
-      const int r1 = (int)min((long long)(e_unit - s0) * p.unit, (long long)pos + 1);
-      if (r1 == pos + 1) {
-        // These rows include the token's own: it is stored first (by every
-        // head chunk, the same bytes) and then read like any other.
-        const size_t row = bh * p.S + pos;
-        if (warp == 0)
-          store_row<T, D, true>(static_cast<const T*>(p.k_t) + bh * D, p.k_codes + row * (D / 2),
-                                p.k_scale + row * (D / 16), lane);
-        else if (warp == 1)
-          store_row<T, D, false>(static_cast<const T*>(p.v_t) + bh * D, p.v_codes + row * (D / 2),
-                                 p.v_scale + row * (D / 16), lane);
-        __syncthreads();
-      }
-      R ring(p, smem + warp * R::kStages * R::kSlot, bh * p.S + r0, r1 - r0, lane);
-#pragma unroll
-      for (int e = 0; e < R::kStages; ++e) {
-        const int r = warp * R::kRows + e * kTurn;
-        if (r < ring.n) ring.fill(e, r);
-        ring.commit();
-      }
-      Attention<D, NP, kTiles> at;
-      at.init(q_t, ng, lane);
-      int slot = 0;
-      for (int r = warp * R::kRows; r < ring.n; r += kTurn) {
-        ring.wait();
-        __syncwarp();
-        at.step(ring, slot, ring.n - r);
-        __syncwarp();  // every lane has read the slot
-        const int ahead = r + R::kStages * kTurn;
-        if (ahead < ring.n) ring.fill(slot, ahead);
-        ring.commit();
-        slot = slot + 1 < R::kStages ? slot + 1 : 0;
-      }
-      __syncthreads();  // the sums below lie where the rings were
-      // This warp's (max, sum, acc) of heads 2c, 2c + 1.
-      const float unit = exp2f((float)at.pe);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        at.l[h] = column_sum(at.l[h]);
-        if (i == 0) {
-          red[warp][2 * c + h][D] = at.m[h];
-          red[warp][2 * c + h][D + 1] = at.l[h];
-        }
-#pragma unroll
-        for (int j = 0; j < D / 32; ++j) {
-          const float add = column_sum(at.omin[j][h]);
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float* to = &red[warp][2 * c + h][32 * j + 4 * i + 2 * k];
-            to[0] = at.o[2 * j + k][h] * at.kUnit1 * unit + add;
-            to[1] = at.o[2 * j + k][2 + h] * (at.kUnit1 * at.kOdd) * unit + add;
-          }
-        }
-      }
-      __syncthreads();
-      const size_t base = k_first == k_last ? head0 : (size_t)p.B * p.H_q + ((size_t)cta * 2 + !first) * kHeads;
-      for (int x = threadIdx.x; x < ng * D; x += kThreads) {
-        const int hh = x / D, e = x - hh * D;
-        float mx = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, red[w][hh][D]);
-        float ls = 0.f, as = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          // A warp without rows has m = -inf, l = acc = 0.
-          const float f = red[w][hh][D] == -INFINITY ? 0.f : exp2_approx(red[w][hh][D] - mx);
-          ls = fmaf(red[w][hh][D + 1], f, ls);
-          as = fmaf(red[w][hh][e], f, as);
-        }
-        float* part = p.part + (base + hh) * (D + 2);
-        part[2 + e] = as;
-        if (e == 0) {
-          part[0] = mx;
-          part[1] = ls;
-        }
-      }
-    } else {
-      // ---------------------------------------------- retrieval
-      // Warp w sums every kWarps-th group of 16 of M's rows, lane l columns
-      // l + 32 k.
-      float(*sq)[D] = reinterpret_cast<float(*)[D]>(smem);  // [kHeads][D], before the sums
-      for (int x = threadIdx.x; x < kHeads * D; x += kThreads) {
-        const int hh = x / D, e = x - hh * D;
-        sq[hh][e] = hh < ng ? elu1(to_f32<T>(q_t[(size_t)hh * D + e])) : 0.f;
-      }
-      __syncthreads();
-      const float* zv = p.z + bh * D;
-      const float* Mh = p.M + bh * D * D;
-      float* ret = p.ret + head0 * (D + 1);
-      for (int hh = warp; hh < ng; hh += kWarps) {
-        float dp = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) dp = fmaf(sq[hh][lane + 32 * e], zv[lane + 32 * e], dp);
-        dp = warp_sum(dp);
-        if (lane == 0) ret[(size_t)hh * (D + 1) + D] = dp;
-      }
-      float acc[kHeads][E];
-#pragma unroll
-      for (int hh = 0; hh < kHeads; ++hh)
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[hh][e] = 0.f;
-      constexpr int kRowsPerWarp = D / kWarps;
-#pragma unroll 8
-      for (int k = 0; k < kRowsPerWarp; ++k) {
-        const int row = warp * kRowsPerWarp + k;
-        float mrow[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) mrow[e] = Mh[(size_t)row * D + lane + 32 * e];
-#pragma unroll
-        for (int hh = 0; hh < kHeads; ++hh) {
-          const float w = sq[hh][row];
-#pragma unroll
-          for (int e = 0; e < E; ++e) acc[hh][e] = fmaf(w, mrow[e], acc[hh][e]);
-        }
-      }
-      __syncthreads();  // sq has been read
-#pragma unroll
-      for (int hh = 0; hh < kHeads; ++hh)
-#pragma unroll
-        for (int e = 0; e < E; ++e) red[warp][hh][lane + 32 * e] = acc[hh][e];
-      __syncthreads();
-      for (int x = threadIdx.x; x < ng * D; x += kThreads) {
-        const int hh = x / D, e = x - hh * D;
-        float num = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) num += red[w][hh][e];
-        ret[(size_t)hh * (D + 1) + e] = num;
-      }
+  Share share;
+  Run run;
+  locate(p, segs, share, run.b, run.off);
+  if (blockIdx.x >= share.ctas) return;
+  const uint32_t u_end = share.first(blockIdx.x + 1);
+  run.end = share.first(blockIdx.x);
+  R ring;
+  Attention<D, NP> at;
+#pragma unroll 1
+  for (bool first = true;; first = false) {
+    // The next run: from run.end, to its segment's end or this CTA's.
+    run.u = run.end;
+    uint32_t n = stream_units(p, run.b);
+    while (run.u >= run.off + segs * n) {
+      run.off += segs * n;
+      n = stream_units(p, ++run.b);
     }
+    run.seg = (run.u - run.off) / n;
+    run.s0 = run.off + run.seg * n + p.lead;
+    run.s1 = run.s0 + n - p.lead;
+    run.end = min(u_end, run.s1);
+    run.u = max(run.u, run.s0);
+    if (run.u >= run.end) return;  // only of a segment's lead: its rows are the next CTA's
+    run.pos = p.pos[run.b];
+    run.hk = run.seg / zc;
+    run.hq0 = run.hk * g + (run.seg - run.hk * zc) * kHeads;
+    run.ng = min(kHeads, (run.hk + 1) * g - run.hq0);
+    const int r0 = (run.u - run.s0) * p.unit;
+    const int r1 = (int)min((long long)(run.end - run.s0) * p.unit, (long long)run.pos + 1);
+    if (r1 == run.pos + 1 && (run.pos - r0) / R::kRows % kWarps == warp) {
+      // The warp that will read the token's own row stores it first (with
+      // several head chunks each does, the same bytes).
+      const size_t row = run.bh(p) * p.S + run.pos;
+      store_row<T, D, true>(static_cast<const T*>(p.k_t) + run.bh(p) * D, p.k_codes + row * (D / 2),
+                            p.k_scale + row * (D / 16), lane);
+      store_row<T, D, false>(static_cast<const T*>(p.v_t) + run.bh(p) * D, p.v_codes + row * (D / 2),
+                             p.v_scale + row * (D / 16), lane);
+      __syncwarp();
+    }
+    ring.set(p, smem + warp * R::kStages * R::kSlot, run.bh(p) * p.S + r0, r1 - r0, lane);
+    Retrieval<D> mem;
+#pragma unroll
+    for (int e = 0; e < R::kStages - 1; ++e) {
+      const int r = warp * R::kRows + e * kTurn;
+      if (r < ring.n) ring.fill(e, r);
+      if (e == R::kStages - 2) mem.template begin<T>(p, run, smem + kRingBytes<D>);
+      R::commit();
+    }
+    at.init(static_cast<const T*>(p.q_t) + run.head0(p) * D, run.ng, lane);
+    at.run(ring, warp);
 
-    // ------------------------------------------------ the last CTA finishes
-    __threadfence();  // this thread's workspace writes, before the ticket
+    // This run's partial: of a CTA that has the segment whole, at the heads' own
+    // place; of others, at the CTA's (its first run, or its last).
+    Partial<D>* part = reinterpret_cast<Partial<D>*>(p.part) +
+                       (run.whole() ? run.head0(p)
+                                    : (size_t)p.B * p.H_q + ((size_t)blockIdx.x * 2 + !first) * kHeads);
+    R::template wait<0>();
     __syncthreads();
-    unsigned int* ctr = p.ctr + (size_t)b * segs + seg;
-    if (threadIdx.x == 0) last = atomicAdd(ctr, 1u) == k_last - k_first + 1;
+    mem.end(part, run.ng);
     __syncthreads();
-    if (last) {
-      __threadfence();  // every other CTA's writes of this segment are visible
-      // Partial x of head hh (x = 0 .. k_last - k_first): only the first CTA of
-      // several may have had another segment before this one.
-      const bool later = k_first != k_last && share.first(k_first) != s0;
-      auto partial = [&](uint32_t x, int hh) {
-        const size_t at = k_first == k_last ? head0
-                                            : (size_t)p.B * p.H_q +
-                                                  ((size_t)(k_first + x) * 2 + (x == 0 && later)) * kHeads;
-        return p.part + (at + hh) * (D + 2);
-      };
-      const int np = k_last - k_first + 1;
-      for (int hh = warp; hh < ng; hh += kWarps) {
-        // A warp merges a head's partials, in CTA order; lane l columns l + 32 e.
-        const float* ret = p.ret + (head0 + hh) * (D + 1);
-        float num[E];
+    // This warp's (max, sum, acc) of heads 2c, 2c + 1.
+    const float unit = exp2f((float)at.pe);
 #pragma unroll
-        for (int e = 0; e < E; ++e) num[e] = __ldcg(ret + lane + 32 * e);
-        const float den = __ldcg(ret + D);
-        const float gm = gate_sigmoid(p.beta[hq0 + hh]);
-        float mx = -INFINITY, ls = 0.f, as[E];
+    for (int h = 0; h < 2; ++h) {
+      at.l[h] = column_sum(at.l[h]);
+      if (i == 0) {
+        red[warp][2 * c + h][D] = at.m[h];
+        red[warp][2 * c + h][D + 1] = at.l[h];
+      }
 #pragma unroll
-        for (int e = 0; e < E; ++e) as[e] = 0.f;
-        constexpr int kU = 8;  // partials in flight
-        for (int c0 = 0; c0 < np; c0 += kU) {
-          float mc[kU], lc[kU], ac[kU][E];
+      for (int j = 0; j < D / 32; ++j) {
+        const float add = column_sum(at.omin[j][h]);
 #pragma unroll
-          for (int x = 0; x < kU; ++x) {
-            const bool in = c0 + x < np;
-            const float* pc = partial(in ? c0 + x : 0, hh);
-            mc[x] = in ? __ldcg(pc) : -INFINITY;
-            lc[x] = in ? __ldcg(pc + 1) : 0.f;
-#pragma unroll
-            for (int e = 0; e < E; ++e) ac[x][e] = in ? __ldcg(pc + 2 + lane + 32 * e) : 0.f;
-          }
-          float nm = mx;
-#pragma unroll
-          for (int x = 0; x < kU; ++x) nm = fmaxf(nm, mc[x]);
-          const float corr = exp2_approx(mx - nm);  // 0 for the first partials
-          ls *= corr;
-#pragma unroll
-          for (int e = 0; e < E; ++e) as[e] *= corr;
-#pragma unroll
-          for (int x = 0; x < kU; ++x) {
-            const float f = exp2_approx(mc[x] - nm);  // 0 past the last partial
-            ls = fmaf(lc[x], f, ls);
-#pragma unroll
-            for (int e = 0; e < E; ++e) as[e] = fmaf(ac[x][e], f, as[e]);
-          }
-          mx = nm;
-        }
-        T* out = static_cast<T*>(p.out_t) + (head0 + hh) * D;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float a_mem = den != 0.f ? num[e] / den : 0.f;
-          out[lane + 32 * e] = from_f32<T>(gm * a_mem + (1.f - gm) * (as[e] / ls));
+        for (int k = 0; k < 2; ++k) {
+          float* to = &red[warp][2 * c + h][32 * j + 4 * i + 2 * k];
+          to[0] = at.o[2 * j + k][h] * at.kUnit1 * unit + add;
+          to[1] = at.o[2 * j + k][2 + h] * (at.kUnit1 * at.kOdd) * unit + add;
         }
       }
-      if (threadIdx.x == 0) *ctr = 0u;  // ready for the next step
     }
-    u = e_unit;
-    if (attend && u < u_end) {
-      __syncthreads();  // `last` and the sums have been read
-      while (u >= off + segs * stream_units(p, b)) off += segs * stream_units(p, b++);
+    __syncthreads();
+#pragma unroll 1
+    for (int x = threadIdx.x; x < run.ng * D; x += kThreads) {
+      const int hh = x / D, e = x - hh * D;
+      float mx = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, red[w][hh][D]);
+      float ls = 0.f, as = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        // A warp without rows has m = -inf, l = acc = 0.
+        const float f = red[w][hh][D] == -INFINITY ? 0.f : exp2_approx(red[w][hh][D] - mx);
+        ls = fmaf(red[w][hh][D + 1], f, ls);
+        as = fmaf(red[w][hh][e], f, as);
+      }
+      part[hh].acc[e] = as;
+      if (e == 0) {
+        part[hh].m = mx;
+        part[hh].l = ls;
+      }
     }
+    finish<T, D>(p, share, run, segs);  // (its barriers also free the sums)
+    if (run.end >= u_end) return;
   }
 }
 
@@ -1000,15 +1110,15 @@ int chunks_of(int g) { return (g + kHeads - 1) / kHeads; }
 // units, one per CTA, none across a segment's end; with more work the units are
 // 128 rows and every CTA takes an equal run of them.
 struct Q4Plan {
-  int unit;
-  long long ctas, segments;
+  int unit, lead;
+  long long ctas;
 };
 Q4Plan q4_plan(int B, int H_q, int H_kv, int S) {
   const long long segments = (long long)B * H_kv * chunks_of(H_q / H_kv), most = kSMs * kResident;
   const long long units = segments * ((S + kUnit - 1) / kUnit);
-  if (units > 2 * most) return {kUnit, most, segments};
+  if (units > 2 * most) return {kUnit, kLeadUnits, most};
   const int per = (int)((units + most - 1) / most);
-  return {per * kUnit, segments * ((S + per * kUnit - 1) / (per * kUnit)), segments};
+  return {per * kUnit, 0, segments * ((S + per * kUnit - 1) / (per * kUnit))};
 }
 
 template <typename T, int D>
@@ -1016,18 +1126,18 @@ cudaError_t launch(const Q4Problem& p, Q4What what, int n, void* k, void* v, cud
   const dim3 rows((unsigned)(((long long)n * (D / 8) + kThreads - 1) / kThreads), p.B * p.H_kv, 2);
   switch (what) {
     case Q4What::kStep: {
-      using R = Ring<D, Parts<T>::n == 1 ? 2 : 1>;
-      constexpr int ring = kWarps * R::kStages * R::kSlot, sums = kWarps * kHeads * (D + 2) * 4;
-      constexpr int bytes = ring > sums ? ring : sums;
-#ifdef QS
-      if (bytes > 48 * 1024) cudaFuncSetAttribute(q4_decode_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-#endif
+      constexpr int bytes = kSmemBytes<D>;
+      if (bytes > 48 * 1024) {
+        cudaError_t e =
+            cudaFuncSetAttribute(q4_decode_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) return e;
+      }
       const Q4Plan plan = q4_plan(p.B, p.H_q, p.H_kv, p.S);
       Q4Problem q = p;
-      q.ctas = plan.ctas;
+      q.ctas = (int)plan.ctas;
       q.unit = plan.unit;
-      q4_decode_kernel<T, D>
-          <<<(unsigned)(plan.ctas + plan.segments), kThreads, bytes, st>>>(q);
+      q.lead = plan.lead;
+      q4_decode_kernel<T, D><<<(unsigned)plan.ctas, kThreads, bytes, st>>>(q);
       break;
     }
     case Q4What::kAppend: q4_append_kernel<T, D><<<rows, kThreads, 0, st>>>(p, n); break;
@@ -1052,9 +1162,9 @@ cudaError_t launch_type(const Q4Problem& p, Q4What what, int n, void* k, void* v
 
 int q4_head_chunks(int g) { return chunks_of(g); }
 
-// Partials: one per query head, and two sets of kHeads per CTA.
-size_t q4_partials(int B, int H_q, int H_kv, int S) {
-  return (size_t)B * H_q + (size_t)q4_plan(B, H_q, H_kv, S).ctas * 2 * kHeads;
+// Bytes of the partials: one per query head, and two sets of kHeads per CTA.
+size_t q4_partial_bytes(int B, int H_q, int H_kv, int S, int d) {
+  return ((size_t)B * H_q + (size_t)q4_plan(B, H_q, H_kv, S).ctas * 2 * kHeads) * (d + kThreads + 4) * 4;
 }
 
 cudaError_t launch_q4(const Q4Problem& p, Q4What what, int n, void* k, void* v, cudaStream_t st) {
