@@ -46,14 +46,11 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kHeads = 8;               // query heads of a CTA (columns of a product)
 constexpr int kUnit = kWarps * 32;      // rows of the smallest share of the work
 constexpr int kSMs = 148;
-#ifndef QB
-#define QB 3
-#endif
-#ifndef QL
-#define QL 4
-#endif
-constexpr int kLeadUnits = QL;
-constexpr int kResident = QB;  // CTAs per SM (bf16 heads; two for fp32 ones)
+// What a segment costs besides its rows, in units of 128 rows (the latencies of
+// its first loads and its partial's way to the workspace): 64 streams at ragged
+// positions below 8192 take 145 us with 2, 121 with 4, 105 with 8, 112 with 12.
+constexpr int kLeadUnits = 8;
+constexpr int kResident = 3;  // CTAs per SM (bf16 heads; two for fp32 ones)
 
 template <int BYTES> struct RawBytes;
 template <> struct RawBytes<2> { using type = unsigned short; };
@@ -101,9 +98,9 @@ __device__ __forceinline__ float column_max(float x) {
 // 8 channels 8 w .. 8 w + 7 of a row, held by one lane, into the buffer; the 4
 // lanes of a 32-channel group are neighbours and call together.  fp32
 // arithmetic with one rounding per operation; a group with a NaN becomes NaN.
-template <int D, bool KEY>
-__device__ __forceinline__ void store_group(const float (&x)[8], int w, uint8_t* codes, __nv_bfloat16* sm,
-                                            bool active) {
+template <int D>
+__device__ __forceinline__ void store_group(const float (&x)[8], int w, bool key, uint8_t* codes,
+                                            __nv_bfloat16* sm, bool active) {
   constexpr int NJ = D / 32;
   const int j = w >> 2, c = w & 3;
   float lo = x[0], hi = x[0];
@@ -151,7 +148,7 @@ __device__ __forceinline__ void store_group(const float (&x)[8], int w, uint8_t*
     }
   }
   if (!active) return;
-  if constexpr (KEY) {
+  if (key) {
     uint32_t word = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) word |= q[e] << ((e & 1) ? 2 * e + 14 : 2 * e);
@@ -197,13 +194,16 @@ __device__ __forceinline__ void store8(float* x, const float (&v)[8]) {
   reinterpret_cast<float4*>(x)[1] = {v[4], v[5], v[6], v[7]};
 }
 
-// One row x[0..D-1] into the buffer, by one warp (D / 8 of its lanes).
-template <typename T, int D, bool KEY>
-__device__ __forceinline__ void store_row(const T* x, uint8_t* codes, __nv_bfloat16* sm, int lane) {
-  const bool active = lane < D / 8;
+// The token's key and value into row `row` of the buffer, by one warp: half of
+// it for each.
+template <typename T, int D>
+__device__ __forceinline__ void store_token(const Q4Problem& p, size_t bh, size_t row, int lane) {
+  const bool key = lane < 16, active = (lane & 15) < D / 8;
+  const int w = lane & 15 & (D / 8 - 1);
   float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (active) load8(x + 8 * lane, v);
-  store_group<D, KEY>(v, lane & (D / 8 - 1), codes, sm, active);
+  if (active) load8(static_cast<const T*>(key ? p.k_t : p.v_t) + bh * D + 8 * w, v);
+  store_group<D>(v, w, key, (key ? p.k_codes : p.v_codes) + row * (D / 2),
+                 (key ? p.k_scale : p.v_scale) + row * (D / 16), active);
 }
 
 // fp16 parts that hold a query or a probability of this type.
@@ -240,14 +240,16 @@ struct Ring {
   static constexpr int kRows = 16;
   static constexpr int kCodes = kRows * (D / 2), kParams = kRows * (D / 8);  // bytes of a slot's rows
   static constexpr int kSlot = 2 * kCodes + 2 * kParams;
-#ifdef QS
-  static constexpr int kStages = QS;
-#else
   static constexpr int kStages = 4;
-#endif
+  // The ring first carries the warp's rows of the memory M, kMem at a time.
+  static constexpr int kMem = kSlot / (D * 4);
+  static_assert(kMem * D * 4 == kSlot, "whole rows");
   uint8_t* smem;
   const uint8_t *k, *v, *kp, *vp;  // the first row
+  const float* mem;                // the warp's first row of M
   int n, lane;                     // rows
+  int mem_rows, mem_items;
+  int first;                       // the warp's first row behind them
 
   __device__ __forceinline__ void set(const Q4Problem& p, uint8_t* ring, size_t row0, int rows, int lane_) {
     smem = ring; n = rows; lane = lane_;
@@ -298,7 +300,21 @@ struct Ring {
     if (__builtin_expect(r + kRows <= n, 1)) fill_rows<true>(slot, r);
     else fill_rows<false>(slot, r);
   }
-  __device__ __forceinline__ static void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  // Starts the copy of the warp's item x: kMem rows of M, or 16 rows.
+  __device__ __forceinline__ void next(int slot, int x) const {
+    if (x >= mem_items) {
+      const int r = first + (x - mem_items) * kWarps * kRows;
+      if (r < n) fill(slot, r);
+    } else {
+      const uint32_t s = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + slot * kSlot;
+      const uint8_t* src = reinterpret_cast<const uint8_t*>(mem + (size_t)x * kMem * D);
+      const int bytes = min(kMem, mem_rows - x * kMem) * D * 4;
+#pragma unroll
+      for (int e = 0; e < kSlot; e += 512)
+        if (e + lane * 16 < bytes) copy<16>(s + e + lane * 16, src + e + lane * 16);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
   // Waits until at most LEFT groups of this lane are in flight.
   template <int LEFT>
   __device__ __forceinline__ static void wait() {
@@ -474,9 +490,6 @@ struct Attention {
       for (int part = 0; part < NP; ++part)
 #pragma unroll
         for (int k = 0; k < 4; ++k) qf[j][part][k] = split_f16(x[j][2 * k], x[j][2 * k + 1]);
-      omin[j][0] = omin[j][1] = 0.f;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) o[2 * j][k] = o[2 * j + 1][k] = 0.f;
     }
     // This lane's indexes along the minima: 2c, 2c + 1 (b0), 2c + 8, 2c + 9 (b1).
     {
@@ -502,6 +515,17 @@ struct Attention {
     f1 = rsqrtf((float)D) * 1.4426950408889634f * kUnit1;
     f2[0] = pow2(-__shfl_sync(0xffffffffu, e, 8 * c));
     f2[1] = pow2(-__shfl_sync(0xffffffffu, e, 8 * c + 4));
+    clear();
+  }
+
+  // Before the first row.
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      omin[j][0] = omin[j][1] = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[2 * j][k] = o[2 * j + 1][k] = 0.f;
+    }
     m[0] = m[1] = -INFINITY;
     l[0] = l[1] = 0.f;
     pe = -120;
@@ -621,38 +645,36 @@ struct Attention {
     l[1] += pr[1] + pr[3];
   }
 
-  // All of a ring's rows of this warp (every kWarps-th 16).  A turn computes one
-  // tile's scores and the tile before's products with the values: two chains
-  // that do not wait for each other, in the code of one tile.
-  __device__ __forceinline__ void run(const Ring<D>& ring, int warp) {
+  // All of a ring's rows of this warp (every kWarps-th 16), from item mem_items
+  // on, which lies in `slot`.  A turn computes one tile's scores and the tile
+  // before's products with the values: two chains that do not wait for each
+  // other, in the code of one tile.
+  __device__ __forceinline__ void run(const Ring<D>& ring, int slot) {
     using R = Ring<D>;
-    constexpr int kTurn = kWarps * R::kRows;
     const int kr = k_row(ring.lane >> 2);
     float pr[4] = {0.f, 0.f, 0.f, 0.f};
-    int slot = 0, before = R::kStages - 1;
-    for (int r = warp * R::kRows; r < ring.n; r += kTurn) {
-      // Of the kStages groups before this turn's the first is needed; the slot
-      // of two tiles ago is free, the one of the tile before is read below.
+    int before = slot > 0 ? slot - 1 : R::kStages - 1, x = ring.mem_items;
+#pragma unroll 1
+    for (int r = ring.first; r < ring.n; r += kWarps * R::kRows, ++x) {
+      // Of the kStages - 1 groups before this turn's the first is needed; the
+      // slot of the tile before is read below and filled again.
       R::template wait<R::kStages - 2>();
       KeyTile<D> keys;
       ring.read(keys, slot);
-      float x[4];
-      scores(keys, ring.n - r, kr, x);
+      float s[4];
+      scores(keys, ring.n - r, kr, s);
       ValueTile<D> val;
-      if (r >= kTurn) {
+      if (r > ring.first) {
         ring.read(val, before);
         values(val, pr);
         __syncwarp();  // every lane has read the slot
       }
-      const int ahead = r + (R::kStages - 1) * kTurn;
-      if (ahead < ring.n) ring.fill(before, ahead);
-      R::commit();
-      const uint32_t top = ring.top_scale(slot);
-      probabilities(x, top, pr);
+      ring.next(before, x + R::kStages - 1);
+      probabilities(s, ring.top_scale(slot), pr);
       before = slot;
       slot = slot + 1 < R::kStages ? slot + 1 : 0;
     }
-    if (warp * R::kRows < ring.n) {
+    if (ring.first < ring.n) {
       ValueTile<D> val;
       ring.read(val, before);
       values(val, pr);
@@ -693,48 +715,36 @@ struct Share {
   }
 };
 
-// Adds up the streams' units (the whole CTA calls it), shares them out, and
-// finds the stream that this CTA's first unit lies in, and its first unit.
+// Adds up the streams' units, shares them out, and finds the stream that this
+// CTA's first unit lies in, and the stream's first unit.  Every warp does it for
+// itself, 32 streams at a time: no barrier.
 __device__ __forceinline__ void locate(const Q4Problem& p, uint32_t segs, Share& share, uint32_t& stream,
                                        uint32_t& start) {
-  __shared__ uint32_t sums[kWarps], found[2];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int per = (p.B + kThreads - 1) / kThreads, b0 = min((int)threadIdx.x * per, p.B), b1 = min(b0 + per, p.B);
-  uint32_t mine = 0;
+  const int lane = threadIdx.x & 31;
+  uint32_t total = 0, mine = 0;
 #pragma unroll 1
-  for (int b = b0; b < b1; ++b) mine += stream_units(p, b) * segs;
-  uint32_t incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
-  }
-  if (lane == 31) sums[warp] = incl;
-  __syncthreads();
-  uint32_t total = 0, at = incl - mine;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) at += sums[w];
-    total += sums[w];
-  }
-  share.set(total, p.ctas);
+  for (int b = lane; b < p.B; b += 32) total += mine = stream_units(p, b) * segs;
+  share.set(__reduce_add_sync(0xffffffffu, total), p.ctas);
   if (blockIdx.x >= share.ctas) return;
   const uint32_t want = share.first(blockIdx.x);
-  if (want >= at && want < at + mine) {
+  start = 0;
 #pragma unroll 1
-    for (int b = b0; b < b1; ++b) {
-      const uint32_t n = stream_units(p, b) * segs;
-      if (want < at + n) {
-        found[0] = b;
-        found[1] = at;
-        break;
-      }
-      at += n;
+  for (int b0 = 0;; b0 += 32) {
+    if (p.B > 32) mine = b0 + lane < p.B ? stream_units(p, b0 + lane) * segs : 0;
+    uint32_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
     }
+    const uint32_t behind = __ballot_sync(0xffffffffu, want < start + incl);
+    if (behind) {  // the first such lane's stream (`want` lies below the total)
+      stream = b0 + __ffs(behind) - 1;
+      start += __shfl_sync(0xffffffffu, incl - mine, __ffs(behind) - 1);
+      return;
+    }
+    start += __shfl_sync(0xffffffffu, incl, 31);
   }
-  __syncthreads();
-  stream = found[0];
-  start = found[1];
 }
 
 // A run of units of one segment, and the segment's place.
@@ -749,21 +759,35 @@ struct Run {
 };
 
 // What a CTA leaves of a run, per head: the attention over its rows (max
-// reference m, sum l, acc[D]) and its share of the retrieval, sigma(q) M in
-// kThreads / D parts and sigma(q) z.
+// reference m, sum l, acc[D]) and its share of the retrieval, sigma(q) M and
+// sigma(q) z.
 template <int D>
 struct Partial {
   float acc[D];
-  float num[kThreads];
-  float m, l, den, unused;
+  float num[D];
+  float m, l, den, unused;  // 16 bytes, read as one
 };
+
+// E neighbouring floats that another CTA wrote.
+template <int E>
+__device__ __forceinline__ void load_columns(const float* p, float (&x)[E]) {
+  if constexpr (E == 4) {
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(p));
+    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+  } else if constexpr (E == 2) {
+    const float2 v = __ldcg(reinterpret_cast<const float2*>(p));
+    x[0] = v.x; x[1] = v.y;
+  } else {
+    x[0] = __ldcg(p);
+  }
+}
 
 // The ticket of a segment, taken once a CTA's share of it is in the workspace;
 // the last CTA merges the partials in CTA order, with the gate.  The whole CTA
 // calls it; no CTA waits for another.
 template <typename T, int D>
 __device__ __forceinline__ void finish(const Q4Problem& p, const Share& share, const Run& r, uint32_t segs) {
-  constexpr int E = D / 32;  // channels per lane
+  constexpr int E = D / 32, kU = 8;  // channels per lane; partials in flight
   __shared__ int last;       // partials to merge, 0 if this CTA is not the last
   __shared__ uint32_t first_cta;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -788,34 +812,41 @@ __device__ __forceinline__ void finish(const Q4Problem& p, const Share& share, c
   const Partial<D>* mine = part + (np == 1 ? head0 : (size_t)p.B * p.H_q + (size_t)first_cta * 2 * kHeads);
   for (int hh = warp; hh < r.ng; hh += kWarps) {
     auto at = [&](int x) { return mine + (size_t)x * 2 * kHeads + (x == 0 && later ? kHeads : 0) + hh; };
-    float mx = -INFINITY;
-#pragma unroll 1
-    for (int x = lane; x < np; x += 32) mx = fmaxf(mx, __ldcg(&at(x)->m));
-    mx = warp_max(mx);
-    float ls = 0.f, den = 0.f, as[E], num[E];
+    // 32 partials a turn: (m, l, den) one per lane, and 8 at a time every lane's
+    // E columns (E l .. E l + E - 1), the first 8 before the weights are needed.
+    float mx = -INFINITY, ls = 0.f, den = 0.f, w = 0.f, as[E], num[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) as[e] = num[e] = 0.f;
 #pragma unroll 1
-    for (int x0 = 0; x0 < np; x0 += 32) {
-      float w = 0.f, lx = 0.f, dx = 0.f;
-      if (x0 + lane < np) {
-        const Partial<D>* q = at(x0 + lane);
-        w = exp2_approx(__ldcg(&q->m) - mx);
-        lx = __ldcg(&q->l) * w;
-        dx = __ldcg(&q->den);
+    for (int k0 = 0; k0 < np; k0 += kU) {
+      const bool turn = k0 % 32 == 0;
+      float4 t = {-INFINITY, 0.f, 0.f, 0.f};
+      if (turn && k0 + lane < np) t = __ldcg(reinterpret_cast<const float4*>(&at(k0 + lane)->m));
+      float av[kU][E], nv[kU][E];
+#pragma unroll
+      for (int k = 0; k < kU; ++k) {
+        const Partial<D>* q = at(min(k0 + k, np - 1));
+        load_columns<E>(q->acc + E * lane, av[k]);
+        load_columns<E>(q->num + E * lane, nv[k]);
       }
-      ls += warp_sum(lx);
-      den += warp_sum(dx);
-      const int n = min(32, np - x0);
-#pragma unroll 4
-      for (int k = 0; k < n; ++k) {
-        const Partial<D>* q = at(x0 + k);
-        const float wk = __shfl_sync(0xffffffffu, w, k);
+      if (turn) {
+        const float nm = fmaxf(mx, warp_max(t.x)), corr = exp2_approx(mx - nm);  // 0 for the first
+        w = exp2_approx(t.x - nm);  // 0 past the last
+        mx = nm;
+        ls = fmaf(ls, corr, warp_sum(t.y * w));
+        den += warp_sum(t.z);
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          as[e] = fmaf(__ldcg(&q->acc[lane + 32 * e]), wk, as[e]);
+        for (int e = 0; e < E; ++e) as[e] *= corr;
+      }
 #pragma unroll
-          for (int u = 0; u < kThreads / D; ++u) num[e] += __ldcg(&q->num[u * D + lane + 32 * e]);
+      for (int k = 0; k < kU; ++k) {
+        const float wk = __shfl_sync(0xffffffffu, w, (k0 + k) & 31);
+        if (k0 + k < np) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            as[e] = fmaf(av[k][e], wk, as[e]);
+            num[e] += nv[k][e];
+          }
         }
       }
     }
@@ -824,105 +855,66 @@ __device__ __forceinline__ void finish(const Q4Problem& p, const Share& share, c
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       const float a_mem = den != 0.f ? num[e] / den : 0.f;
-      out[lane + 32 * e] = from_f32<T>(gm * a_mem + (1.f - gm) * (as[e] / ls));
+      out[E * lane + e] = from_f32<T>(gm * a_mem + (1.f - gm) * (as[e] / ls));
     }
   }
   if (threadIdx.x == 0) *ctr = 0u;  // ready for the next step
 }
 
-// A CTA's share of the retrieval: sigma(q) M and sigma(q) z over M's rows [k0,
-// k1), which the CTAs of a segment split as they split its rows.  The first 32
-// of them are copied to shared memory while the rows are attended to.
+// A warp's share of the retrieval: its rows of M, which come through the ring
+// before the segment's, times sigma(q) (sq: of the warp's first row on), to
+// num[kHeads][D].  Returns the slot behind them.
 template <int D>
-struct Retrieval {
-  static constexpr int kRows = 32;
-  static constexpr int kBytes = (kRows * D + D * kHeads) * 4;
-  float* buf;             // [kRows][D]
-  float (*sq)[kHeads];    // [D]: sigma(q), k0's first
-  int k0, k1;
-  const float* M;
-  float den;              // sigma(q) z of this thread's head
-  __device__ __forceinline__ void copy(int k) const {
-    const int n = min(kRows, k1 - k) * D / 4;  // 16-byte pieces
-#pragma unroll 2
-    for (int x = threadIdx.x; x < n; x += kThreads) {
-      const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(buf + 4 * x));
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(M + (size_t)k * D + 4 * x) : "memory");
-    }
-  }
-  template <typename T>
-  __device__ __forceinline__ void begin(const Q4Problem& p, const Run& r, uint8_t* smem) {
-    buf = reinterpret_cast<float*>(smem);
-    sq = reinterpret_cast<float(*)[kHeads]>(buf + kRows * D);
-    // By units: the runs of a segment tile its rows, and M's with them.
-    const uint32_t n = r.s1 - r.s0;
-    k0 = (int)((unsigned long long)(r.u - r.s0) * D / n);
-    k1 = (int)((unsigned long long)(r.end - r.s0) * D / n);
-    M = p.M + r.bh(p) * D * D;
-    copy(k0);
-    // sigma(q) and its product with z: 16 threads a head, all loads first.
-    const int hh = threadIdx.x / 16, t = threadIdx.x % 16;
-    const T* q = static_cast<const T*>(p.q_t) + (r.head0(p) + (hh < r.ng ? hh : 0)) * D + k0;
-    const float* z = p.z + r.bh(p) * D + k0;
-    float qv[D / 16], zv[D / 16];
+__device__ __forceinline__ int retrieve(const Ring<D>& ring, const float (*sq)[kHeads], float (*num)[D]) {
+  using R = Ring<D>;
+  constexpr int E = D / 32;  // columns E l .. E l + E - 1 of lane l
+  float acc[kHeads][E];
 #pragma unroll
-    for (int e = 0; e < D / 16; ++e) {
-      const bool in = t + 16 * e < k1 - k0;
-      qv[e] = in ? to_f32<T>(q[t + 16 * e]) : 0.f;
-      zv[e] = in ? z[t + 16 * e] : 0.f;
-    }
-    den = 0.f;
+  for (int hh = 0; hh < kHeads; ++hh)
 #pragma unroll
-    for (int e = 0; e < D / 16; ++e) {
-      const float s = elu1(qv[e]);
-      if (t + 16 * e < k1 - k0) sq[t + 16 * e][hh] = s;
-      den = fmaf(s, zv[e], den);
-    }
-#pragma unroll
-    for (int o = 1; o < 16; o <<= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
-  }
-  // After the copies of begin() are waited for and a barrier.
-  __device__ __forceinline__ void end(Partial<D>* part, int ng) const {
-    const int col = threadIdx.x % D, u = threadIdx.x / D;  // this thread's column and part
-    float acc[kHeads];
-#pragma unroll
-    for (int hh = 0; hh < kHeads; ++hh) acc[hh] = 0.f;
-    auto add = [&](int row, float mv) {  // row: relative to k0
-      const float4 lo = *reinterpret_cast<const float4*>(sq[row]);
-      const float4 hi = *reinterpret_cast<const float4*>(sq[row] + 4);
-      acc[0] = fmaf(lo.x, mv, acc[0]); acc[1] = fmaf(lo.y, mv, acc[1]);
-      acc[2] = fmaf(lo.z, mv, acc[2]); acc[3] = fmaf(lo.w, mv, acc[3]);
-      acc[4] = fmaf(hi.x, mv, acc[4]); acc[5] = fmaf(hi.y, mv, acc[5]);
-      acc[6] = fmaf(hi.z, mv, acc[6]); acc[7] = fmaf(hi.w, mv, acc[7]);
-    };
-    constexpr int kStep = kThreads / D, kB = 8;  // rows in flight behind the first 32
-    const int n = min(kRows, k1 - k0);
-#pragma unroll 4
-    for (int x = u; x < n; x += kStep) add(x, buf[x * D + col]);
+    for (int e = 0; e < E; ++e) acc[hh][e] = 0.f;
+  int slot = 0, before = R::kStages - 1;
 #pragma unroll 1
-    for (int x0 = kRows + u; x0 < k1 - k0; x0 += kB * kStep) {
-      float mv[kB];
-#pragma unroll
-      for (int e = 0; e < kB; ++e) {
-        const int x = x0 + e * kStep;
-        mv[e] = x < k1 - k0 ? __ldcs(M + (size_t)(k0 + x) * D + col) : 0.f;
+  for (int x = 0; x < ring.mem_items; ++x) {
+    R::template wait<R::kStages - 2>();
+    ring.next(before, x + R::kStages - 1);  // (read in the turn before)
+    const float* rows = reinterpret_cast<const float*>(ring.smem + slot * R::kSlot) + E * ring.lane;
+    const int n = min(R::kMem, ring.mem_rows - x * R::kMem);
+#pragma unroll 1
+    for (int k = 0; k < n; ++k) {
+      float mv[E];
+      if constexpr (E == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(rows + k * D);
+        mv[0] = v.x; mv[1] = v.y; mv[2] = v.z; mv[3] = v.w;
+      } else if constexpr (E == 2) {
+        const float2 v = *reinterpret_cast<const float2*>(rows + k * D);
+        mv[0] = v.x; mv[1] = v.y;
+      } else {
+        mv[0] = rows[k * D];
       }
+      const float4 lo = *reinterpret_cast<const float4*>(sq[x * R::kMem + k]);
+      const float4 hi = *reinterpret_cast<const float4*>(sq[x * R::kMem + k] + 4);
+      const float w[kHeads] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-      for (int e = 0; e < kB; ++e)
-        if (x0 + e * kStep < k1 - k0) add(x0 + e * kStep, mv[e]);
+      for (int hh = 0; hh < kHeads; ++hh)
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[hh][e] = fmaf(w[hh], mv[e], acc[hh][e]);
     }
-#pragma unroll
-    for (int hh = 0; hh < kHeads; ++hh)
-      if (hh < ng) part[hh].num[threadIdx.x] = acc[hh];
-    if (threadIdx.x % 16 == 0 && (int)threadIdx.x / 16 < ng) part[threadIdx.x / 16].den = den;
+    __syncwarp();  // every lane has read the slot
+    before = slot;
+    slot = slot + 1 < R::kStages ? slot + 1 : 0;
   }
-};
+#pragma unroll
+  for (int hh = 0; hh < kHeads; ++hh)
+#pragma unroll
+    for (int e = 0; e < E; ++e) num[hh][E * ring.lane + e] = acc[hh][e];
+  return slot;
+}
 
 template <int D> constexpr int kRingBytes = kWarps * Ring<D>::kStages * Ring<D>::kSlot;
 template <int D> constexpr int kSumBytes = kWarps * kHeads * (D + 2) * 4;
-// The sums lie where the retrieval's rows were.
-template <int D>
-constexpr int kSmemBytes = kRingBytes<D> + (kSumBytes<D> > Retrieval<D>::kBytes ? kSumBytes<D> : Retrieval<D>::kBytes);
+template <int D> constexpr int kNumBytes = kWarps * kHeads * D * 4;
+template <int D> constexpr int kSmemBytes = kRingBytes<D> + kSumBytes<D> + kNumBytes<D>;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, Parts<T>::n == 1 ? kResident : 2)
@@ -933,6 +925,8 @@ q4_decode_kernel(Q4Problem p) {
   constexpr int kTurn = kWarps * R::kRows;  // rows the CTA's warps take at a time
   extern __shared__ __align__(16) uint8_t smem[];
   float(*red)[kHeads][D + 2] = reinterpret_cast<float(*)[kHeads][D + 2]>(smem + kRingBytes<D>);  // [kWarps]
+  float(*sq)[kHeads] = reinterpret_cast<float(*)[kHeads]>(smem + kRingBytes<D>);  // [D], before the sums
+  float(*num)[kHeads][D] = reinterpret_cast<float(*)[kHeads][D]>(smem + kRingBytes<D> + kSumBytes<D>);  // [kWarps]
 
   const int g = p.H_q / p.H_kv, zc = (g + kHeads - 1) / kHeads;
   const uint32_t segs = (uint32_t)(p.H_kv * zc);
@@ -952,101 +946,137 @@ q4_decode_kernel(Q4Problem p) {
   run.end = share.first(blockIdx.x);
   R ring;
   Attention<D, NP> at;
+  float den = 0.f;  // sigma(q) z over the run's rows of M, of head threadIdx.x / 16
+  at.clear();
 #pragma unroll 1
-  for (bool first = true;; first = false) {
-    // The next run: from run.end, to its segment's end or this CTA's.
+  for (int turn = 0;; ++turn) {
+    // The next run: from run.end, to its segment's end or this CTA's.  Its rows
+    // are on their way before the last one is put away.
+    const Run done = run;
     run.u = run.end;
-    uint32_t n = stream_units(p, run.b);
-    while (run.u >= run.off + segs * n) {
-      run.off += segs * n;
-      n = stream_units(p, ++run.b);
-    }
-    run.seg = (run.u - run.off) / n;
-    run.s0 = run.off + run.seg * n + p.lead;
-    run.s1 = run.s0 + n - p.lead;
-    run.end = min(u_end, run.s1);
-    run.u = max(run.u, run.s0);
-    if (run.u >= run.end) return;  // only of a segment's lead: its rows are the next CTA's
-    run.pos = p.pos[run.b];
-    run.hk = run.seg / zc;
-    run.hq0 = run.hk * g + (run.seg - run.hk * zc) * kHeads;
-    run.ng = min(kHeads, (run.hk + 1) * g - run.hq0);
-    const int r0 = (run.u - run.s0) * p.unit;
-    const int r1 = (int)min((long long)(run.end - run.s0) * p.unit, (long long)run.pos + 1);
-    if (r1 == run.pos + 1 && (run.pos - r0) / R::kRows % kWarps == warp) {
-      // The warp that will read the token's own row stores it first (with
-      // several head chunks each does, the same bytes).
-      const size_t row = run.bh(p) * p.S + run.pos;
-      store_row<T, D, true>(static_cast<const T*>(p.k_t) + run.bh(p) * D, p.k_codes + row * (D / 2),
-                            p.k_scale + row * (D / 16), lane);
-      store_row<T, D, false>(static_cast<const T*>(p.v_t) + run.bh(p) * D, p.v_codes + row * (D / 2),
-                             p.v_scale + row * (D / 16), lane);
-      __syncwarp();
-    }
-    ring.set(p, smem + warp * R::kStages * R::kSlot, run.bh(p) * p.S + r0, r1 - r0, lane);
-    Retrieval<D> mem;
-#pragma unroll
-    for (int e = 0; e < R::kStages - 1; ++e) {
-      const int r = warp * R::kRows + e * kTurn;
-      if (r < ring.n) ring.fill(e, r);
-      if (e == R::kStages - 2) mem.template begin<T>(p, run, smem + kRingBytes<D>);
-      R::commit();
-    }
-    at.init(static_cast<const T*>(p.q_t) + run.head0(p) * D, run.ng, lane);
-    at.run(ring, warp);
-
-    // This run's partial: of a CTA that has the segment whole, at the heads' own
-    // place; of others, at the CTA's (its first run, or its last).
-    Partial<D>* part = reinterpret_cast<Partial<D>*>(p.part) +
-                       (run.whole() ? run.head0(p)
-                                    : (size_t)p.B * p.H_q + ((size_t)blockIdx.x * 2 + !first) * kHeads);
-    R::template wait<0>();
-    __syncthreads();
-    mem.end(part, run.ng);
-    __syncthreads();
-    // This warp's (max, sum, acc) of heads 2c, 2c + 1.
-    const float unit = exp2f((float)at.pe);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      at.l[h] = column_sum(at.l[h]);
-      if (i == 0) {
-        red[warp][2 * c + h][D] = at.m[h];
-        red[warp][2 * c + h][D + 1] = at.l[h];
+    bool more = run.end < u_end;
+    int k0 = 0, k1 = 0;
+    if (more) {
+      uint32_t n = stream_units(p, run.b);
+      while (run.u >= run.off + segs * n) {
+        run.off += segs * n;
+        n = stream_units(p, ++run.b);
       }
+      run.seg = (run.u - run.off) / n;
+      n -= p.lead;
+      run.s0 = run.off + run.seg * (n + p.lead) + p.lead;
+      run.s1 = run.s0 + n;
+      run.end = min(u_end, run.s1);
+      run.u = max(run.u, run.s0);
+      more = run.u < run.end;  // (else only of a segment's lead: its rows are the next CTA's)
+      if (more) {
+        run.pos = p.pos[run.b];
+        run.hk = zc == 1 ? run.seg : run.seg / zc;
+        run.hq0 = run.hk * g + (run.seg - run.hk * zc) * kHeads;
+        run.ng = min(kHeads, (run.hk + 1) * g - run.hq0);
+        const int r0 = (run.u - run.s0) * p.unit;
+        const int r1 = (int)min((long long)(run.end - run.s0) * p.unit, (long long)run.pos + 1);
+        if (r1 == run.pos + 1 && (run.pos - r0) / R::kRows % kWarps == warp) {
+          // The warp that will read the token's own row stores it first (with
+          // several head chunks each does, the same bytes).
+          store_token<T, D>(p, run.bh(p), run.bh(p) * p.S + run.pos, lane);
+          __syncwarp();
+        }
+        // M's rows k0 .. k1 - 1 go with the run's units, a quarter to each warp.
+        k0 = (run.u - run.s0) * D / n;  // (at most 2^30 / 128 units)
+        k1 = (run.end - run.s0) * D / n;
+        const int w0 = (k1 - k0) * warp / kWarps, w1 = (k1 - k0) * (warp + 1) / kWarps;
+        ring.set(p, smem + warp * R::kStages * R::kSlot, run.bh(p) * p.S + r0, r1 - r0, lane);
+        ring.mem = p.M + (run.bh(p) * D + k0 + w0) * D;
+        ring.mem_rows = w1 - w0;
+        ring.mem_items = (w1 - w0 + R::kMem - 1) / R::kMem;
+        ring.first = warp * R::kRows;
+#pragma unroll 1
+        for (int e = 0; e < R::kStages - 1; ++e) ring.next(e, e);
+      }
+    }
+
+    if (turn > 0) {
+      // The last run's partial: of a CTA that has the segment whole, at the
+      // heads' own place; of others, at the CTA's (its first run, or its last).
+      Partial<D>* part = reinterpret_cast<Partial<D>*>(p.part) +
+                         (done.whole() ? done.head0(p)
+                                       : (size_t)p.B * p.H_q + ((size_t)blockIdx.x * 2 + (turn > 1)) * kHeads);
+      if (threadIdx.x % 16 == 0 && (int)threadIdx.x / 16 < done.ng) part[threadIdx.x / 16].den = den;
+      __syncthreads();  // sigma(q) has been read
+      // This warp's (max, sum, acc) of heads 2c, 2c + 1.
+      const float unit = exp2f((float)at.pe);
 #pragma unroll
-      for (int j = 0; j < D / 32; ++j) {
-        const float add = column_sum(at.omin[j][h]);
+      for (int h = 0; h < 2; ++h) {
+        at.l[h] = column_sum(at.l[h]);
+        if (i == 0) {
+          red[warp][2 * c + h][D] = at.m[h];
+          red[warp][2 * c + h][D + 1] = at.l[h];
+        }
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          float* to = &red[warp][2 * c + h][32 * j + 4 * i + 2 * k];
-          to[0] = at.o[2 * j + k][h] * at.kUnit1 * unit + add;
-          to[1] = at.o[2 * j + k][2 + h] * (at.kUnit1 * at.kOdd) * unit + add;
+        for (int j = 0; j < D / 32; ++j) {
+          const float add = column_sum(at.omin[j][h]);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float* to = &red[warp][2 * c + h][32 * j + 4 * i + 2 * k];
+            to[0] = at.o[2 * j + k][h] * at.kUnit1 * unit + add;
+            to[1] = at.o[2 * j + k][2 + h] * (at.kUnit1 * at.kOdd) * unit + add;
+          }
         }
       }
+      __syncthreads();
+#pragma unroll 1
+      for (int x = threadIdx.x; x < done.ng * D; x += kThreads) {
+        const int hh = x / D, e = x - hh * D;
+        float mx = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, red[w][hh][D]);
+        float ls = 0.f, as = 0.f, ns = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          // A warp without rows has m = -inf, l = acc = 0.
+          const float f = red[w][hh][D] == -INFINITY ? 0.f : exp2_approx(red[w][hh][D] - mx);
+          ls = fmaf(red[w][hh][D + 1], f, ls);
+          as = fmaf(red[w][hh][e], f, as);
+          ns += num[w][hh][e];
+        }
+        part[hh].acc[e] = as;
+        part[hh].num[e] = ns;
+        if (e == 0) {
+          part[hh].m = mx;
+          part[hh].l = ls;
+        }
+      }
+      finish<T, D>(p, share, done, segs);  // (its barriers also free the sums)
+    }
+    if (!more) return;
+
+    // sigma(q) and its product with z: 16 threads a head, all loads first.
+    {
+      const int hh = threadIdx.x / 16, t = threadIdx.x % 16;
+      const T* q = static_cast<const T*>(p.q_t) + (run.head0(p) + (hh < run.ng ? hh : 0)) * D + k0;
+      const float* z = p.z + run.bh(p) * D + k0;
+      float qv[D / 16], zv[D / 16];
+#pragma unroll
+      for (int e = 0; e < D / 16; ++e) {
+        const bool in = t + 16 * e < k1 - k0;
+        qv[e] = in ? to_f32<T>(q[t + 16 * e]) : 0.f;
+        zv[e] = in ? z[t + 16 * e] : 0.f;
+      }
+      at.init(static_cast<const T*>(p.q_t) + run.head0(p) * D, run.ng, lane);
+      den = 0.f;
+#pragma unroll
+      for (int e = 0; e < D / 16; ++e) {
+        const float s = elu1(qv[e]);
+        if (t + 16 * e < k1 - k0) sq[t + 16 * e][hh] = s;
+        den = fmaf(s, zv[e], den);
+      }
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
     }
     __syncthreads();
-#pragma unroll 1
-    for (int x = threadIdx.x; x < run.ng * D; x += kThreads) {
-      const int hh = x / D, e = x - hh * D;
-      float mx = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, red[w][hh][D]);
-      float ls = 0.f, as = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        // A warp without rows has m = -inf, l = acc = 0.
-        const float f = red[w][hh][D] == -INFINITY ? 0.f : exp2_approx(red[w][hh][D] - mx);
-        ls = fmaf(red[w][hh][D + 1], f, ls);
-        as = fmaf(red[w][hh][e], f, as);
-      }
-      part[hh].acc[e] = as;
-      if (e == 0) {
-        part[hh].m = mx;
-        part[hh].l = ls;
-      }
-    }
-    finish<T, D>(p, share, run, segs);  // (its barriers also free the sums)
-    if (run.end >= u_end) return;
+    const int slot = retrieve<D>(ring, sq + (k1 - k0) * warp / kWarps, num[warp]);
+    at.run(ring, slot);
   }
 }
 
@@ -1069,10 +1099,8 @@ __global__ void __launch_bounds__(kThreads) q4_append_kernel(Q4Problem p, int n)
   float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   if (active) load8(src, v);
   const size_t row = (size_t)bh * p.S + pos + t;
-  if (key)
-    store_group<D, true>(v, w, p.k_codes + row * (D / 2), p.k_scale + row * (D / 16), active);
-  else
-    store_group<D, false>(v, w, p.v_codes + row * (D / 2), p.v_scale + row * (D / 16), active);
+  store_group<D>(v, w, key, (key ? p.k_codes : p.v_codes) + row * (D / 2),
+                 (key ? p.k_scale : p.v_scale) + row * (D / 16), active);
 }
 
 // The values of rows 0..n-1 as k and v [B, H_kv, n, D]: a thread writes 8
@@ -1164,7 +1192,7 @@ int q4_head_chunks(int g) { return chunks_of(g); }
 
 // Bytes of the partials: one per query head, and two sets of kHeads per CTA.
 size_t q4_partial_bytes(int B, int H_q, int H_kv, int S, int d) {
-  return ((size_t)B * H_q + (size_t)q4_plan(B, H_q, H_kv, S).ctas * 2 * kHeads) * (d + kThreads + 4) * 4;
+  return ((size_t)B * H_q + (size_t)q4_plan(B, H_q, H_kv, S).ctas * 2 * kHeads) * (2 * d + 4) * 4;
 }
 
 cudaError_t launch_q4(const Q4Problem& p, Q4What what, int n, void* k, void* v, cudaStream_t st) {
