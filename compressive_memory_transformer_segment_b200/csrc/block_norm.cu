@@ -16,9 +16,12 @@
 // not depend on the row.
 //
 // Bound by memory: each stream is read once and each result written once, so
-// a row stays in registers between its two reductions.  One CTA per row at a
-// time, 16 bytes per thread and stream (element by element where D makes the
-// rows unaligned); every statistic and sum in fp32.
+// a row stays in registers between its two reductions.  One CTA takes a row at a
+// time, 16 bytes per thread and stream (4 bytes, or single elements, where D
+// makes the rows unaligned), and walks over the rows with its columns' weights in
+// registers.  Its next rows are on their way meanwhile: every thread copies its
+// own pieces to shared memory asynchronously (so no barrier goes with them) and
+// reads them back when their turn comes.  All statistics and sums in fp32.
 #include "common.cuh"
 #include "kernels.h"
 #include "pdl.cuh"
@@ -29,32 +32,19 @@ namespace {
 
 constexpr int kSMs = 148;
 constexpr int kMaxThreads = 512;
-constexpr int kRegThreads = 512;  // threads per SM at the backward's register count
+constexpr int kFwdThreads = 1024;  // threads per SM that the registers allow
+constexpr int kBwdThreads = 512;
 
 template <int BYTES> struct RawVec;
 template <> struct RawVec<2> { using type = unsigned short; };
 template <> struct RawVec<4> { using type = unsigned int; };
 template <> struct RawVec<16> { using type = uint4; };
 
-// Streams pass through once: they stay out of L1, which keeps the weights.
-__device__ __forceinline__ void ld_stream(const void* p, uint4& r) {
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
-}
-__device__ __forceinline__ void ld_stream(const void* p, unsigned int& r) {
-  asm volatile("ld.global.L1::no_allocate.u32 %0, [%1];" : "=r"(r) : "l"(p));
-}
-__device__ __forceinline__ void ld_stream(const void* p, unsigned short& r) {
-  asm volatile("ld.global.L1::no_allocate.u16 %0, [%1];" : "=h"(r) : "l"(p));
-}
-
 // V consecutive elements of T, as loaded.
 template <typename T, int V>
 struct Pack {
-  typename RawVec<V * (int)sizeof(T)>::type raw;
-  __device__ __forceinline__ void load(const void* base, size_t at) {
-    ld_stream(static_cast<const T*>(base) + at, raw);
-  }
+  static constexpr int kBytes = V * (int)sizeof(T);
+  typename RawVec<kBytes>::type raw;
   __device__ __forceinline__ void clear() { raw = {}; }
   __device__ __forceinline__ float get(int i) const {
     return to_f32<T>(reinterpret_cast<const T*>(&raw)[i]);
@@ -65,10 +55,66 @@ struct Pack {
   }
 };
 
-// V consecutive fp32 weights; 1 where the vector is absent.
+// A thread's pieces of a row's streams: N vectors of each of ARRAYS streams, with
+// STAGES - 1 rows on their way (STAGES = 1: loaded when they are needed, which
+// 2-byte pieces have to be).
+template <typename T, int V, int N, int ARRAYS, int STAGES>
+struct Streams {
+  using P = Pack<T, V>;
+  uint8_t* smem;             // this thread's first piece
+  const void* base[ARRAYS];  // null: not there (reads as zero)
+  size_t width;
+  int nvec;
+  __device__ __forceinline__ uint8_t* at(int stage, int a, int i) const {
+    return smem + (size_t)((stage * ARRAYS + a) * N + i) * blockDim.x * P::kBytes;
+  }
+  __device__ __forceinline__ const uint8_t* source(int a, long long row, int i) const {
+    return static_cast<const uint8_t*>(base[a]) +
+           ((size_t)row * width + (size_t)(threadIdx.x + i * blockDim.x) * V) * sizeof(T);
+  }
+  __device__ __forceinline__ void start(int stage, long long row, long long rows) const {
+    if constexpr (STAGES > 1) {
+      if (row < rows) {
+#pragma unroll
+        for (int a = 0; a < ARRAYS; ++a)
+          if (base[a]) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+              if (threadIdx.x + i * blockDim.x < nvec) {
+                const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(at(stage, a, i)));
+                if constexpr (P::kBytes == 16)
+                  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(source(a, row, i))
+                               : "memory");
+                else
+                  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(source(a, row, i))
+                               : "memory");
+              }
+          }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+  }
+  __device__ __forceinline__ static void wait() {
+    if constexpr (STAGES > 1) asm volatile("cp.async.wait_group %0;" ::"n"(STAGES > 1 ? STAGES - 2 : 0) : "memory");
+  }
+  __device__ __forceinline__ void read(int stage, long long row, P (&x)[ARRAYS][N]) const {
+#pragma unroll
+    for (int a = 0; a < ARRAYS; ++a)
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        x[a][i].clear();
+        if (base[a] && threadIdx.x + i * blockDim.x < nvec) {
+          const uint8_t* from = STAGES > 1 ? at(stage, a, i) : source(a, row, i);
+          x[a][i].raw = *reinterpret_cast<const decltype(x[a][i].raw)*>(from);
+        }
+      }
+  }
+};
+
+// V consecutive fp32 weights; 1 where the vector is absent or `in` is false.
 template <int V>
-__device__ __forceinline__ void load_weights(const float* w, int at, float (&x)[V]) {
-  if (w == nullptr) {
+__device__ __forceinline__ void load_weights(const float* w, int at, bool in, float (&x)[V]) {
+  if (w == nullptr || !in) {
 #pragma unroll
     for (int i = 0; i < V; ++i) x[i] = 1.f;
   } else if constexpr (V % 4 == 0) {
@@ -82,6 +128,33 @@ __device__ __forceinline__ void load_weights(const float* w, int at, float (&x)[
     for (int i = 0; i < V; ++i) x[i] = __ldg(w + at + i);
   }
 }
+
+// A thread's columns of a weight vector: in registers for the kernel's whole life
+// where MOST of them fit, read for every row otherwise.
+template <int V, int N, int MOST>
+struct Weights {
+  static constexpr bool kKept = N * V <= MOST;
+  const float* w;
+  float kept[kKept ? N : 1][V];
+  __device__ __forceinline__ void load(const float* w_, int nvec) {
+    w = w_;
+    if constexpr (kKept) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int v = threadIdx.x + i * blockDim.x;
+        load_weights<V>(w, v * V, v < nvec, kept[i]);
+      }
+    }
+  }
+  __device__ __forceinline__ void get(int i, float (&x)[V]) const {
+    if constexpr (kKept) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) x[e] = kept[i][e];
+    } else {
+      load_weights<V>(w, (threadIdx.x + i * blockDim.x) * V, true, x);
+    }
+  }
+};
 
 // Logistic of a gate logit, u, and 1 - u (as e^-a u, which keeps its digits
 // where u rounds to 1).  0 and 1 in the limits, NaN for NaN; the bound only
@@ -107,31 +180,43 @@ __device__ __forceinline__ float block_sum(float x, float (*slots)[32], int& tur
   return x;
 }
 
+// Rows in flight: by a thread's bytes of one row, so that the rings of an SM's
+// CTAs fit into its shared memory (512 threads of 96 bytes take 4 x 48 KB).
+constexpr int stages_of(int bytes, bool copies) { return !copies ? 1 : bytes <= 96 ? 4 : bytes <= 192 ? 2 : 1; }
+
+// (512 threads that hold one vector each: two CTAs an SM; the registers of wider
+// rows leave room for one.)
 template <typename T, int V, int N>
-__global__ void __launch_bounds__(kMaxThreads)
+__global__ void __launch_bounds__(kMaxThreads, N == 1 ? 2 : 1)
 block_norm_fwd_kernel(BlockNormProblem p) {
+  constexpr int STAGES = stages_of(3 * N * V * (int)sizeof(T), V * sizeof(T) >= 4);
   __shared__ float slots[2][32];
+  extern __shared__ __align__(16) uint8_t ring[];
   int turn = 0;
   const int D = p.width, nvec = D / V;
   const float inv_d = 1.f / (float)D;
-  for (long long row = blockIdx.x; row < p.rows; row += gridDim.x) {
-    const size_t base = (size_t)row * D;
-    Pack<T, V> r[N], o[N], a[N];
+  using S = Streams<T, V, N, 3, STAGES>;
+  S in = {ring + threadIdx.x * S::P::kBytes, {p.r, p.o, p.gate}, (size_t)D, nvec};
+  Weights<V, N, 16> wp, wc, wn;
+  wp.load(p.w_post, nvec);
+  wc.load(p.scale, nvec);
+  wn.load(p.w_next, nvec);
+  const long long step = gridDim.x;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int v = threadIdx.x + i * blockDim.x;
-      r[i].clear(); o[i].clear(); a[i].clear();
-      if (v < nvec) {
-        r[i].load(p.r, base + (size_t)v * V);
-        if (p.o) o[i].load(p.o, base + (size_t)v * V);
-        if (p.gate) a[i].load(p.gate, base + (size_t)v * V);
-      }
-    }
+  for (int s = 0; s < STAGES - 1; ++s) in.start(s, blockIdx.x + s * step, p.rows);
+  int stage = 0;
+  for (long long row = blockIdx.x; row < p.rows; row += step) {
+    const size_t base = (size_t)row * D;
+    typename S::P raw[3][N];  // r, o, gate
+    S::wait();
+    in.read(stage, row, raw);
+    in.start(stage > 0 ? stage - 1 : STAGES - 1, row + (STAGES - 1) * step, p.rows);
+    stage = stage + 1 < STAGES ? stage + 1 : 0;
     float x[N][V];
 #pragma unroll
     for (int i = 0; i < N; ++i)
 #pragma unroll
-      for (int e = 0; e < V; ++e) x[i][e] = r[i].get(e);
+      for (int e = 0; e < V; ++e) x[i][e] = raw[0][i].get(e);
     if (p.o) {
       float rp = 1.f;
       if (p.w_post) {
@@ -139,7 +224,7 @@ block_norm_fwd_kernel(BlockNormProblem p) {
 #pragma unroll
         for (int i = 0; i < N; ++i)
 #pragma unroll
-          for (int e = 0; e < V; ++e) ss = fmaf(o[i].get(e), o[i].get(e), ss);
+          for (int e = 0; e < V; ++e) ss = fmaf(raw[1][i].get(e), raw[1][i].get(e), ss);
         rp = rsqrtf(block_sum(ss, slots, turn) * inv_d + p.eps);
         if (p.rstd_post && threadIdx.x == 0) p.rstd_post[row] = rp;
       }
@@ -147,15 +232,15 @@ block_norm_fwd_kernel(BlockNormProblem p) {
       for (int i = 0; i < N; ++i) {
         const int v = threadIdx.x + i * blockDim.x;
         if (v < nvec) {
-          float wp[V], c[V];
-          load_weights<V>(p.w_post, v * V, wp);
-          load_weights<V>(p.scale, v * V, c);
-          Pack<T, V> out;
+          float post[V], c[V];
+          wp.get(i, post);
+          wc.get(i, c);
+          typename S::P out;
 #pragma unroll
           for (int e = 0; e < V; ++e) {
             float rest;
-            const float u = p.gate ? sigmoid(a[i].get(e), rest) : 1.f;
-            x[i][e] = fmaf(o[i].get(e) * rp * wp[e], u * c[e], x[i][e]);
+            const float u = p.gate ? sigmoid(raw[2][i].get(e), rest) : 1.f;
+            x[i][e] = fmaf(raw[1][i].get(e) * rp * post[e], u * c[e], x[i][e]);
             out.set(e, x[i][e]);
           }
           out.store(p.r_out, base + (size_t)v * V);
@@ -176,11 +261,11 @@ block_norm_fwd_kernel(BlockNormProblem p) {
       for (int i = 0; i < N; ++i) {
         const int v = threadIdx.x + i * blockDim.x;
         if (v < nvec) {
-          float wn[V];
-          load_weights<V>(p.w_next, v * V, wn);
-          Pack<T, V> out;
+          float next[V];
+          wn.get(i, next);
+          typename S::P out;
 #pragma unroll
-          for (int e = 0; e < V; ++e) out.set(e, x[i][e] * rn * wn[e]);
+          for (int e = 0; e < V; ++e) out.set(e, x[i][e] * rn * next[e]);
           out.store(p.h, base + (size_t)v * V);
         }
       }
@@ -188,67 +273,57 @@ block_norm_fwd_kernel(BlockNormProblem p) {
   }
 }
 
-// One row's streams of the backward.
-template <typename T, int V, int N>
-struct BwdRow {
-  Pack<T, V> dr[N], dh[N], x[N], o[N], a[N];
-  __device__ __forceinline__ void load(const BlockNormProblem& p, long long row, int nvec) {
-    const size_t base = (size_t)row * p.width;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int v = threadIdx.x + i * blockDim.x;
-      dr[i].clear(); dh[i].clear(); x[i].clear(); o[i].clear(); a[i].clear();
-      if (v < nvec) {
-        const size_t at = base + (size_t)v * V;
-        if (p.dr_out) dr[i].load(p.dr_out, at);
-        if (p.w_next) {
-          dh[i].load(p.dh, at);
-          x[i].load(p.r, at);
-        }
-        if (p.o) o[i].load(p.o, at);
-        if (p.gate) a[i].load(p.gate, at);
-      }
-    }
-  }
-};
-
 template <typename T, int V, int N>
 __global__ void __launch_bounds__(kMaxThreads, 1)
 block_norm_bwd_kernel(BlockNormProblem p) {
+  constexpr int STAGES = stages_of(5 * N * V * (int)sizeof(T), V * sizeof(T) >= 4);
   __shared__ float slots[2][32];
+  extern __shared__ __align__(16) uint8_t ring[];
   int turn = 0;
   const int D = p.width, nvec = D / V;
   const float inv_d = 1.f / (float)D;
   const bool want_a = p.scale || p.w_post;
+  using S = Streams<T, V, N, 5, STAGES>;
+  S in = {ring + threadIdx.x * S::P::kBytes,
+          {p.dr_out, p.dh, p.w_next ? p.r : nullptr, p.o, p.gate}, (size_t)D, nvec};
+  Weights<V, N, 8> wp, wc, wn;  // (the sums take as many registers)
+  wp.load(p.w_post, nvec);
+  wc.load(p.scale, nvec);
+  wn.load(p.w_next, nvec);
   float acc_n[N][V], acc_a[N][V];  // this CTA's rows' shares of dw_next and A
 #pragma unroll
   for (int i = 0; i < N; ++i)
 #pragma unroll
     for (int e = 0; e < V; ++e) acc_n[i][e] = acc_a[i][e] = 0.f;
-
-  BwdRow<T, V, N> cur;
-  if (blockIdx.x < p.rows) cur.load(p, blockIdx.x, nvec);
-  for (long long row = blockIdx.x; row < p.rows; row += gridDim.x) {
+  const long long step = gridDim.x;
+#pragma unroll
+  for (int s = 0; s < STAGES - 1; ++s) in.start(s, blockIdx.x + s * step, p.rows);
+  int stage = 0;
+  for (long long row = blockIdx.x; row < p.rows; row += step) {
     const size_t base = (size_t)row * D;
+    typename S::P raw[5][N];  // dr_out, dh, r_out, o, gate
+    const float rn = p.w_next ? p.rstd_next[row] : 0.f, rp = p.w_post ? p.rstd_post[row] : 1.f;
+    S::wait();
+    in.read(stage, row, raw);
+    in.start(stage > 0 ? stage - 1 : STAGES - 1, row + (STAGES - 1) * step, p.rows);
+    stage = stage + 1 < STAGES ? stage + 1 : 0;
     float G[N][V];
 #pragma unroll
     for (int i = 0; i < N; ++i)
 #pragma unroll
-      for (int e = 0; e < V; ++e) G[i][e] = cur.dr[i].get(e);
+      for (int e = 0; e < V; ++e) G[i][e] = raw[0][i].get(e);
     if (p.w_next) {
-      const float rn = p.rstd_next[row];
       float dot = 0.f;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const int v = threadIdx.x + i * blockDim.x;
-        if (v < nvec) {
-          float wn[V];
-          load_weights<V>(p.w_next, v * V, wn);
+        if (threadIdx.x + i * blockDim.x < nvec) {
+          float next[V];
+          wn.get(i, next);
 #pragma unroll
           for (int e = 0; e < V; ++e) {
-            const float n = cur.x[i].get(e) * rn, dh = cur.dh[i].get(e);
+            const float n = raw[2][i].get(e) * rn, dh = raw[1][i].get(e);
             acc_n[i][e] = fmaf(dh, n, acc_n[i][e]);
-            dot = fmaf(dh * wn[e], n, dot);
+            dot = fmaf(dh * next[e], n, dot);
           }
         }
       }
@@ -257,13 +332,13 @@ block_norm_bwd_kernel(BlockNormProblem p) {
       for (int i = 0; i < N; ++i) {
         const int v = threadIdx.x + i * blockDim.x;
         if (v < nvec) {
-          float wn[V];
-          load_weights<V>(p.w_next, v * V, wn);
-          Pack<T, V> out;
+          float next[V];
+          wn.get(i, next);
+          typename S::P out;
 #pragma unroll
           for (int e = 0; e < V; ++e) {
-            const float n = cur.x[i].get(e) * rn;
-            G[i][e] = fmaf(rn, fmaf(-n, m, cur.dh[i].get(e) * wn[e]), G[i][e]);
+            const float n = raw[2][i].get(e) * rn;
+            G[i][e] = fmaf(rn, fmaf(-n, m, raw[1][i].get(e) * next[e]), G[i][e]);
             out.set(e, G[i][e]);
           }
           out.store(p.dr, base + (size_t)v * V);
@@ -271,24 +346,23 @@ block_norm_bwd_kernel(BlockNormProblem p) {
       }
     }
     if (p.o) {
-      const float rp = p.w_post ? p.rstd_post[row] : 1.f;
       float f[N][V], dot = 0.f;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const int v = threadIdx.x + i * blockDim.x;
         if (v < nvec) {
-          float wp[V], c[V];
-          load_weights<V>(p.w_post, v * V, wp);
-          load_weights<V>(p.scale, v * V, c);
-          Pack<T, V> da;
+          float post[V], c[V];
+          wp.get(i, post);
+          wc.get(i, c);
+          typename S::P da;
 #pragma unroll
           for (int e = 0; e < V; ++e) {
             float rest = 0.f;
-            const float u = p.gate ? sigmoid(cur.a[i].get(e), rest) : 1.f;
-            const float n = cur.o[i].get(e) * rp;
+            const float u = p.gate ? sigmoid(raw[4][i].get(e), rest) : 1.f;
+            const float n = raw[3][i].get(e) * rp;
             const float gu = G[i][e] * u;
             acc_a[i][e] = fmaf(gu, n, acc_a[i][e]);
-            f[i][e] = gu * c[e] * wp[e];
+            f[i][e] = gu * c[e] * post[e];
             dot = fmaf(f[i][e], n, dot);
             da.set(e, f[i][e] * n * rest);
           }
@@ -304,15 +378,14 @@ block_norm_bwd_kernel(BlockNormProblem p) {
       for (int i = 0; i < N; ++i) {
         const int v = threadIdx.x + i * blockDim.x;
         if (v < nvec) {
-          Pack<T, V> out;
+          typename S::P out;
 #pragma unroll
           for (int e = 0; e < V; ++e)
-            out.set(e, rp * fmaf(-(cur.o[i].get(e) * rp), m, f[i][e]));
+            out.set(e, rp * fmaf(-(raw[3][i].get(e) * rp), m, f[i][e]));
           out.store(p.d_o, base + (size_t)v * V);
         }
       }
     }
-    if (row + gridDim.x < p.rows) cur.load(p, row + gridDim.x, nvec);
   }
   // Partials [CTA][2][D]; the second kernel adds them in CTA order.
   float* part = p.part + (size_t)blockIdx.x * 2 * D;
@@ -359,105 +432,97 @@ block_norm_reduce_kernel(BlockNormProblem p, int n_part) {
   }
 }
 
-// Threads of a CTA for rows of nvec vectors, N vectors per thread.
-int row_threads(int nvec, int n) {
-  const int t = ((nvec + n - 1) / n + 31) / 32 * 32;
-  return t < kMaxThreads ? t : kMaxThreads;
-}
-
 struct Shape {
-  int vec, n, threads;
+  int vec, n, threads, per_sm;
+  size_t smem;
 };
 
-// 16-byte vectors where the rows are 16-byte aligned, single elements
-// otherwise; as few vectors per thread as kMaxThreads threads need.
-Shape row_shape(int width, int elem) {
+// The widest pieces that the rows' alignment allows; as few of them per thread
+// as kMaxThreads threads need (a power of two); as many CTAs per SM as
+// `sm_threads` threads are (registers), at most 16.
+Shape row_shape(int width, int elem, int arrays, int sm_threads) {
   Shape s;
-  s.vec = (width * elem) % 16 == 0 ? 16 / elem : 1;
+  const int bytes = (width * elem) % 16 == 0 ? 16 : (width * elem) % 4 == 0 ? 4 : 2;
+  s.vec = bytes / elem;
   const int nvec = width / s.vec;
   s.n = 1;
   while (s.n * kMaxThreads < nvec) s.n *= 2;
-  s.threads = row_threads(nvec, s.n);
+  s.threads = ((nvec + s.n - 1) / s.n + 31) / 32 * 32;
+  s.per_sm = sm_threads / (s.n > 1 && sm_threads > kMaxThreads ? 2 : 1) / s.threads;
+  s.per_sm = s.per_sm < 1 ? 1 : s.per_sm > 16 ? 16 : s.per_sm;
+  const int piece = arrays * s.n * bytes, stages = stages_of(piece, bytes >= 4);
+  s.smem = stages > 1 ? (size_t)piece * s.threads * stages : 0;
   return s;
 }
 
-template <typename T, int V>
-cudaError_t launch_fwd(const BlockNormProblem& p, const Shape& s, cudaStream_t st) {
-  const unsigned grid = (unsigned)(p.rows < 0x7fffffffLL ? p.rows : 0x7fffffffLL);
-  switch (s.n) {
-    case 1: block_norm_fwd_kernel<T, V, 1><<<grid, s.threads, 0, st>>>(p); break;
-    case 2: block_norm_fwd_kernel<T, V, 2><<<grid, s.threads, 0, st>>>(p); break;
-    case 4: block_norm_fwd_kernel<T, V, 4><<<grid, s.threads, 0, st>>>(p); break;
-    default:
-      if constexpr (V <= 4) {
-        if (s.n == 8) { block_norm_fwd_kernel<T, V, 8><<<grid, s.threads, 0, st>>>(p); break; }
-      }
-      if constexpr (V == 1) {
-        if (s.n == 16) { block_norm_fwd_kernel<T, V, 16><<<grid, s.threads, 0, st>>>(p); break; }
-        if (s.n == 32) { block_norm_fwd_kernel<T, V, 32><<<grid, s.threads, 0, st>>>(p); break; }
-      }
-      return cudaErrorInvalidValue;
-  }
-  return cudaGetLastError();
-}
-
-template <typename T, int V>
-cudaError_t launch_bwd(const BlockNormProblem& p, const Shape& s, int grid, cudaStream_t st) {
-  switch (s.n) {
-    case 1: block_norm_bwd_kernel<T, V, 1><<<grid, s.threads, 0, st>>>(p); break;
-    case 2: block_norm_bwd_kernel<T, V, 2><<<grid, s.threads, 0, st>>>(p); break;
-    case 4: block_norm_bwd_kernel<T, V, 4><<<grid, s.threads, 0, st>>>(p); break;
-    default:
-      if constexpr (V <= 4) {
-        if (s.n == 8) { block_norm_bwd_kernel<T, V, 8><<<grid, s.threads, 0, st>>>(p); break; }
-      }
-      if constexpr (V == 1) {
-        if (s.n == 16) { block_norm_bwd_kernel<T, V, 16><<<grid, s.threads, 0, st>>>(p); break; }
-        if (s.n == 32) { block_norm_bwd_kernel<T, V, 32><<<grid, s.threads, 0, st>>>(p); break; }
-      }
-      return cudaErrorInvalidValue;
-  }
-  return cudaGetLastError();
-}
-
-int bwd_grid(long long rows, int threads) {
-  const int per_sm = kRegThreads / threads;
-  const long long most = (long long)kSMs * (per_sm < 1 ? 1 : per_sm);
+int row_grid(long long rows, const Shape& s) {
+  const long long most = (long long)kSMs * s.per_sm;
   return (int)(rows < most ? rows : most);
 }
+
+template <typename K>
+cudaError_t run(K kernel, const BlockNormProblem& p, const Shape& s, cudaStream_t st) {
+  if (s.smem + 1024 > 48 * 1024) {  // (some of the default is the sums')
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s.smem);
+    if (e != cudaSuccess) return e;
+  }
+  kernel<<<row_grid(p.rows, s), s.threads, s.smem, st>>>(p);
+  return cudaGetLastError();
+}
+
+template <bool BWD, typename T, int V, int N>
+cudaError_t launch_n(const BlockNormProblem& p, const Shape& s, cudaStream_t st) {
+  if constexpr (BWD) return run(block_norm_bwd_kernel<T, V, N>, p, s, st);
+  else return run(block_norm_fwd_kernel<T, V, N>, p, s, st);
+}
+
+template <bool BWD, typename T, int V>
+cudaError_t launch_v(const BlockNormProblem& p, const Shape& s, cudaStream_t st) {
+  constexpr int kMost = kBlockNormMaxWidth / V / kMaxThreads;  // vectors per thread
+  switch (s.n) {
+    case 1: return launch_n<BWD, T, V, 1>(p, s, st);
+    case 2: return launch_n<BWD, T, V, 2>(p, s, st);
+    case 4: return launch_n<BWD, T, V, 4>(p, s, st);
+    case 8: if constexpr (kMost >= 8) return launch_n<BWD, T, V, 8>(p, s, st); else break;
+    case 16: if constexpr (kMost >= 16) return launch_n<BWD, T, V, 16>(p, s, st); else break;
+    case 32: if constexpr (kMost >= 32) return launch_n<BWD, T, V, 32>(p, s, st); else break;
+  }
+  return cudaErrorInvalidValue;
+}
+
+template <bool BWD>
+cudaError_t launch_any(const BlockNormProblem& p, const Shape& s, cudaStream_t st) {
+  if (p.bf16) {
+    if (s.vec == 8) return launch_v<BWD, __nv_bfloat16, 8>(p, s, st);
+    if (s.vec == 2) return launch_v<BWD, __nv_bfloat16, 2>(p, s, st);
+    return launch_v<BWD, __nv_bfloat16, 1>(p, s, st);
+  }
+  return s.vec == 4 ? launch_v<BWD, float, 4>(p, s, st) : launch_v<BWD, float, 1>(p, s, st);
+}
+
+Shape fwd_shape(int width, int elem) { return row_shape(width, elem, 3, kFwdThreads); }
+Shape bwd_shape(int width, int elem) { return row_shape(width, elem, 5, kBwdThreads); }
 
 }  // namespace
 
 bool block_norm_supported(int width) { return width >= 1 && width <= kBlockNormMaxWidth; }
 
 int block_norm_partials(long long rows, int width) {
-  // The most that any element type and alignment of this width needs.
-  int most = 0;
-  for (int elem = 2; elem <= 4; elem += 2) {
-    const int g = bwd_grid(rows, row_shape(width, elem).threads);
-    most = g > most ? g : most;
-  }
-  return most;
+  // The most that either element type needs.
+  const int a = row_grid(rows, bwd_shape(width, 2)), b = row_grid(rows, bwd_shape(width, 4));
+  return a > b ? a : b;
 }
 
 cudaError_t launch_block_norm_forward(const BlockNormProblem& p, cudaStream_t st) {
-  const Shape s = row_shape(p.width, p.bf16 ? 2 : 4);
-  if (p.bf16)
-    return s.vec > 1 ? launch_fwd<__nv_bfloat16, 8>(p, s, st) : launch_fwd<__nv_bfloat16, 1>(p, s, st);
-  return s.vec > 1 ? launch_fwd<float, 4>(p, s, st) : launch_fwd<float, 1>(p, s, st);
+  return launch_any<false>(p, fwd_shape(p.width, p.bf16 ? 2 : 4), st);
 }
 
 cudaError_t launch_block_norm_backward(const BlockNormProblem& p, cudaStream_t st) {
-  const Shape s = row_shape(p.width, p.bf16 ? 2 : 4);
-  const int grid = bwd_grid(p.rows, s.threads);
-  cudaError_t e;
-  if (p.bf16)
-    e = s.vec > 1 ? launch_bwd<__nv_bfloat16, 8>(p, s, grid, st) : launch_bwd<__nv_bfloat16, 1>(p, s, grid, st);
-  else
-    e = s.vec > 1 ? launch_bwd<float, 4>(p, s, grid, st) : launch_bwd<float, 1>(p, s, grid, st);
+  const Shape s = bwd_shape(p.width, p.bf16 ? 2 : 4);
+  const cudaError_t e = launch_any<true>(p, s, st);
   if (e != cudaSuccess || !(p.w_next || p.scale || p.w_post)) return e;
   return launch_pdl(true, block_norm_reduce_kernel, dim3((p.width + 31) / 32, 2), dim3(32, 32), 0, st, p,
-                    grid);
+                    row_grid(p.rows, s));
 }
 
 }  // namespace infini
