@@ -61,53 +61,65 @@ struct Pack {
 template <typename T, int V, int N, int ARRAYS, int STAGES>
 struct Streams {
   using P = Pack<T, V>;
-  uint8_t* smem;             // this thread's first piece
-  const void* base[ARRAYS];  // null: not there (reads as zero)
-  size_t width;
+  uint8_t* smem;                   // this thread's first piece
+  const uint8_t* next[ARRAYS];     // its place in the row that is started next (null: not there, reads as zero)
+  long long row;                   // that row
   int nvec;
+  __device__ __forceinline__ Streams(uint8_t* ring, const void* const (&base)[ARRAYS], int width) {
+    smem = ring + threadIdx.x * P::kBytes;
+    nvec = width / V;
+    row = blockIdx.x;
+    const size_t off = ((size_t)row * width + (size_t)threadIdx.x * V) * sizeof(T);
+#pragma unroll
+    for (int a = 0; a < ARRAYS; ++a) next[a] = base[a] ? static_cast<const uint8_t*>(base[a]) + off : nullptr;
+  }
   __device__ __forceinline__ uint8_t* at(int stage, int a, int i) const {
     return smem + (size_t)((stage * ARRAYS + a) * N + i) * blockDim.x * P::kBytes;
   }
-  __device__ __forceinline__ const uint8_t* source(int a, long long row, int i) const {
-    return static_cast<const uint8_t*>(base[a]) +
-           ((size_t)row * width + (size_t)(threadIdx.x + i * blockDim.x) * V) * sizeof(T);
+  __device__ __forceinline__ void advance(size_t row_step) {
+#pragma unroll
+    for (int a = 0; a < ARRAYS; ++a)
+      if (next[a]) next[a] += row_step;
+    row += gridDim.x;
   }
-  __device__ __forceinline__ void start(int stage, long long row, long long rows) const {
+  // Starts the next row's copies (row_step: bytes to the row after it).
+  __device__ __forceinline__ void start(int stage, long long rows, size_t row_step) {
     if constexpr (STAGES > 1) {
       if (row < rows) {
 #pragma unroll
         for (int a = 0; a < ARRAYS; ++a)
-          if (base[a]) {
+          if (next[a]) {
 #pragma unroll
             for (int i = 0; i < N; ++i)
               if (threadIdx.x + i * blockDim.x < nvec) {
                 const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(at(stage, a, i)));
+                const uint8_t* from = next[a] + (size_t)i * blockDim.x * P::kBytes;
                 if constexpr (P::kBytes == 16)
-                  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(source(a, row, i))
-                               : "memory");
+                  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
                 else
-                  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(source(a, row, i))
-                               : "memory");
+                  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
               }
           }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
+      advance(row_step);
     }
   }
   __device__ __forceinline__ static void wait() {
     if constexpr (STAGES > 1) asm volatile("cp.async.wait_group %0;" ::"n"(STAGES > 1 ? STAGES - 2 : 0) : "memory");
   }
-  __device__ __forceinline__ void read(int stage, long long row, P (&x)[ARRAYS][N]) const {
+  __device__ __forceinline__ void read(int stage, P (&x)[ARRAYS][N], size_t row_step) {
 #pragma unroll
     for (int a = 0; a < ARRAYS; ++a)
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         x[a][i].clear();
-        if (base[a] && threadIdx.x + i * blockDim.x < nvec) {
-          const uint8_t* from = STAGES > 1 ? at(stage, a, i) : source(a, row, i);
+        if (next[a] && threadIdx.x + i * blockDim.x < nvec) {
+          const uint8_t* from = STAGES > 1 ? at(stage, a, i) : next[a] + (size_t)i * blockDim.x * P::kBytes;
           x[a][i].raw = *reinterpret_cast<const decltype(x[a][i].raw)*>(from);
         }
       }
+    if constexpr (STAGES == 1) advance(row_step);
   }
 };
 
@@ -134,15 +146,25 @@ __device__ __forceinline__ void load_weights(const float* w, int at, bool in, fl
 template <int V, int N, int MOST>
 struct Weights {
   static constexpr bool kKept = N * V <= MOST;
-  const float* w;
+  const float *w, *times;  // times: a second vector, multiplied in
   float kept[kKept ? N : 1][V];
-  __device__ __forceinline__ void load(const float* w_, int nvec) {
+  __device__ __forceinline__ void read(int v, bool in, float (&x)[V]) const {
+    load_weights<V>(w, v * V, in, x);
+    if (times) {
+      float y[V];
+      load_weights<V>(times, v * V, in, y);
+#pragma unroll
+      for (int e = 0; e < V; ++e) x[e] *= y[e];
+    }
+  }
+  __device__ __forceinline__ void load(const float* w_, int nvec, const float* times_ = nullptr) {
     w = w_;
+    times = times_;
     if constexpr (kKept) {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const int v = threadIdx.x + i * blockDim.x;
-        load_weights<V>(w, v * V, v < nvec, kept[i]);
+        read(v, v < nvec, kept[i]);
       }
     }
   }
@@ -151,17 +173,19 @@ struct Weights {
 #pragma unroll
       for (int e = 0; e < V; ++e) x[e] = kept[i][e];
     } else {
-      load_weights<V>(w, (threadIdx.x + i * blockDim.x) * V, true, x);
+      read(threadIdx.x + i * blockDim.x, true, x);
     }
   }
 };
 
 // Logistic of a gate logit, u, and 1 - u (as e^-a u, which keeps its digits
-// where u rounds to 1).  0 and 1 in the limits, NaN for NaN; the bound only
+// where u rounds to 1), by the hardware's approximations of 2^x and 1 / x
+// (relative error 2^-21 together).  0 and 1 in the limits, NaN for NaN; the bound only
 // keeps infinity times 0 out of 1 - u, where u is 0 and wanted as such.
 __device__ __forceinline__ float sigmoid(float a, float& rest) {
-  const float t = __expf(-a);
-  const float u = __fdividef(1.f, 1.f + t);
+  float t, u;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(a * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(u) : "f"(1.f + t));
   rest = fminf(t, 1e30f) * u;
   return u;
 }
@@ -196,21 +220,22 @@ block_norm_fwd_kernel(BlockNormProblem p) {
   const int D = p.width, nvec = D / V;
   const float inv_d = 1.f / (float)D;
   using S = Streams<T, V, N, 3, STAGES>;
-  S in = {ring + threadIdx.x * S::P::kBytes, {p.r, p.o, p.gate}, (size_t)D, nvec};
-  Weights<V, N, 16> wp, wc, wn;
-  wp.load(p.w_post, nvec);
-  wc.load(p.scale, nvec);
+  const void* const from[3] = {p.r, p.o, p.gate};
+  S in(ring, from, D);
+  Weights<V, N, 16> wb, wn;  // wb: scale w_post
+  wb.load(p.w_post, nvec, p.scale);
   wn.load(p.w_next, nvec);
-  const long long step = gridDim.x;
+  const size_t row_step = (size_t)gridDim.x * D * sizeof(T);
 #pragma unroll
-  for (int s = 0; s < STAGES - 1; ++s) in.start(s, blockIdx.x + s * step, p.rows);
+  for (int s = 0; s < STAGES - 1; ++s) in.start(s, p.rows, row_step);
   int stage = 0;
-  for (long long row = blockIdx.x; row < p.rows; row += step) {
-    const size_t base = (size_t)row * D;
+  // This thread's first element of the row, from the start of an array.
+  size_t here = (size_t)blockIdx.x * D + (size_t)threadIdx.x * V;
+  for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, here += (size_t)gridDim.x * D) {
     typename S::P raw[3][N];  // r, o, gate
     S::wait();
-    in.read(stage, row, raw);
-    in.start(stage > 0 ? stage - 1 : STAGES - 1, row + (STAGES - 1) * step, p.rows);
+    in.read(stage, raw, row_step);
+    in.start(stage > 0 ? stage - 1 : STAGES - 1, p.rows, row_step);
     stage = stage + 1 < STAGES ? stage + 1 : 0;
     float x[N][V];
 #pragma unroll
@@ -232,18 +257,17 @@ block_norm_fwd_kernel(BlockNormProblem p) {
       for (int i = 0; i < N; ++i) {
         const int v = threadIdx.x + i * blockDim.x;
         if (v < nvec) {
-          float post[V], c[V];
-          wp.get(i, post);
-          wc.get(i, c);
+          float both[V];
+          wb.get(i, both);
           typename S::P out;
 #pragma unroll
           for (int e = 0; e < V; ++e) {
             float rest;
             const float u = p.gate ? sigmoid(raw[2][i].get(e), rest) : 1.f;
-            x[i][e] = fmaf(raw[1][i].get(e) * rp * post[e], u * c[e], x[i][e]);
+            x[i][e] = fmaf(raw[1][i].get(e) * rp, u * both[e], x[i][e]);
             out.set(e, x[i][e]);
           }
-          out.store(p.r_out, base + (size_t)v * V);
+          out.store(p.r_out, here + (size_t)i * blockDim.x * V);
         }
       }
     }
@@ -266,7 +290,7 @@ block_norm_fwd_kernel(BlockNormProblem p) {
           typename S::P out;
 #pragma unroll
           for (int e = 0; e < V; ++e) out.set(e, x[i][e] * rn * next[e]);
-          out.store(p.h, base + (size_t)v * V);
+          out.store(p.h, here + (size_t)i * blockDim.x * V);
         }
       }
     }
@@ -284,28 +308,33 @@ block_norm_bwd_kernel(BlockNormProblem p) {
   const float inv_d = 1.f / (float)D;
   const bool want_a = p.scale || p.w_post;
   using S = Streams<T, V, N, 5, STAGES>;
-  S in = {ring + threadIdx.x * S::P::kBytes,
-          {p.dr_out, p.dh, p.w_next ? p.r : nullptr, p.o, p.gate}, (size_t)D, nvec};
-  Weights<V, N, 8> wp, wc, wn;  // (the sums take as many registers)
-  wp.load(p.w_post, nvec);
-  wc.load(p.scale, nvec);
+  const void* const from[5] = {p.dr_out, p.dh, p.w_next ? p.r : nullptr, p.o, p.gate};
+  S in(ring, from, D);
+  Weights<V, N, 8> wb, wn;  // (the sums take as many registers); wb: scale w_post
+  wb.load(p.w_post, nvec, p.scale);
   wn.load(p.w_next, nvec);
   float acc_n[N][V], acc_a[N][V];  // this CTA's rows' shares of dw_next and A
 #pragma unroll
   for (int i = 0; i < N; ++i)
 #pragma unroll
     for (int e = 0; e < V; ++e) acc_n[i][e] = acc_a[i][e] = 0.f;
-  const long long step = gridDim.x;
+  const size_t row_step = (size_t)gridDim.x * D * sizeof(T);
 #pragma unroll
-  for (int s = 0; s < STAGES - 1; ++s) in.start(s, blockIdx.x + s * step, p.rows);
+  for (int s = 0; s < STAGES - 1; ++s) in.start(s, p.rows, row_step);
   int stage = 0;
-  for (long long row = blockIdx.x; row < p.rows; row += step) {
-    const size_t base = (size_t)row * D;
+  float rn_next = p.w_next ? p.rstd_next[blockIdx.x] : 0.f, rp_next = p.w_post ? p.rstd_post[blockIdx.x] : 1.f;
+  // This thread's first element of the row, from the start of an array.
+  size_t here = (size_t)blockIdx.x * D + (size_t)threadIdx.x * V;
+  for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, here += (size_t)gridDim.x * D) {
     typename S::P raw[5][N];  // dr_out, dh, r_out, o, gate
-    const float rn = p.w_next ? p.rstd_next[row] : 0.f, rp = p.w_post ? p.rstd_post[row] : 1.f;
+    const float rn = rn_next, rp = rp_next;
+    if (row + gridDim.x < p.rows) {
+      if (p.w_next) rn_next = p.rstd_next[row + gridDim.x];
+      if (p.w_post) rp_next = p.rstd_post[row + gridDim.x];
+    }
     S::wait();
-    in.read(stage, row, raw);
-    in.start(stage > 0 ? stage - 1 : STAGES - 1, row + (STAGES - 1) * step, p.rows);
+    in.read(stage, raw, row_step);
+    in.start(stage > 0 ? stage - 1 : STAGES - 1, p.rows, row_step);
     stage = stage + 1 < STAGES ? stage + 1 : 0;
     float G[N][V];
 #pragma unroll
@@ -341,7 +370,7 @@ block_norm_bwd_kernel(BlockNormProblem p) {
             G[i][e] = fmaf(rn, fmaf(-n, m, raw[1][i].get(e) * next[e]), G[i][e]);
             out.set(e, G[i][e]);
           }
-          out.store(p.dr, base + (size_t)v * V);
+          out.store(p.dr, here + (size_t)i * blockDim.x * V);
         }
       }
     }
@@ -351,9 +380,8 @@ block_norm_bwd_kernel(BlockNormProblem p) {
       for (int i = 0; i < N; ++i) {
         const int v = threadIdx.x + i * blockDim.x;
         if (v < nvec) {
-          float post[V], c[V];
-          wp.get(i, post);
-          wc.get(i, c);
+          float both[V];
+          wb.get(i, both);
           typename S::P da;
 #pragma unroll
           for (int e = 0; e < V; ++e) {
@@ -362,11 +390,11 @@ block_norm_bwd_kernel(BlockNormProblem p) {
             const float n = raw[3][i].get(e) * rp;
             const float gu = G[i][e] * u;
             acc_a[i][e] = fmaf(gu, n, acc_a[i][e]);
-            f[i][e] = gu * c[e] * post[e];
+            f[i][e] = gu * both[e];
             dot = fmaf(f[i][e], n, dot);
             da.set(e, f[i][e] * n * rest);
           }
-          if (p.gate) da.store(p.dgate, base + (size_t)v * V);
+          if (p.gate) da.store(p.dgate, here + (size_t)i * blockDim.x * V);
         } else {
 #pragma unroll
           for (int e = 0; e < V; ++e) f[i][e] = 0.f;
@@ -382,7 +410,7 @@ block_norm_bwd_kernel(BlockNormProblem p) {
 #pragma unroll
           for (int e = 0; e < V; ++e)
             out.set(e, rp * fmaf(-(raw[3][i].get(e) * rp), m, f[i][e]));
-          out.store(p.d_o, base + (size_t)v * V);
+          out.store(p.d_o, here + (size_t)i * blockDim.x * V);
         }
       }
     }
