@@ -432,26 +432,40 @@ block_norm_bwd_kernel(BlockNormProblem p) {
 }
 
 // Column sums of the partials, in a fixed order: thread (x, y) adds every
-// 32nd CTA's share of its column, then the 32 sums are added in turn.
-__global__ void __launch_bounds__(1024)
+// kSumRows-th CTA's share of its column, then a warp adds a column's kSumRows sums.
+// 8 columns a CTA (a 32-byte sector of each partial), so that narrow rows still
+// spread over the GPU and no thread adds more than 37 values.
+constexpr int kSumCols = 8, kSumRows = 64;
+
+__global__ void __launch_bounds__(kSumCols * kSumRows)
 block_norm_reduce_kernel(BlockNormProblem p, int n_part) {
-  __shared__ float sums[32][33];
+  __shared__ float sums[kSumRows][kSumCols + 1];
   pdl_wait();
   const int D = p.width;
-  const int col = blockIdx.x * 32 + threadIdx.x;
+  const int col = blockIdx.x * kSumCols + threadIdx.x;
   const bool second = blockIdx.y == 1;  // 0: dw_next, 1: A
   float s = 0.f;
   if (col < D && (second ? (p.scale || p.w_post) : p.w_next != nullptr)) {
     const float* part = p.part + (second ? D : 0) + col;
-#pragma unroll 8
-    for (int c = threadIdx.y; c < n_part; c += 32) s += __ldcg(part + (size_t)c * 2 * D);
+    constexpr int kU = 12;  // in flight together
+    for (int c0 = threadIdx.y; c0 < n_part; c0 += kU * kSumRows) {
+      float v[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int c = c0 + u * kSumRows;
+        v[u] = c < n_part ? __ldcg(part + (size_t)c * 2 * D) : 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < kU; ++u) s += v[u];
+    }
   }
   sums[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
-  // One warp per column: rows of `sums` transposed, so a warp adds 32 values.
-  const float total = warp_sum(sums[threadIdx.x][threadIdx.y]);
-  const int out = blockIdx.x * 32 + threadIdx.y;
-  if (threadIdx.x != 0 || out >= D) return;
+  const int t = threadIdx.y * kSumCols + threadIdx.x, lane = t & 31, warp = t >> 5;
+  if (warp >= kSumCols) return;
+  const float total = warp_sum(sums[lane][warp] + sums[lane + 32][warp]);
+  const int out = blockIdx.x * kSumCols + warp;
+  if (lane != 0 || out >= D) return;
   if (!second) {
     if (p.dw_next) p.dw_next[out] = total;
   } else {
@@ -465,15 +479,16 @@ struct Shape {
   size_t smem;
 };
 
-// The widest pieces that the rows' alignment allows; as few of them per thread
-// as kMaxThreads threads need (a power of two); as many CTAs per SM as
+// The widest pieces that the rows' alignment allows; one of them per thread up to
+// `one` threads, as few as kMaxThreads threads need (a power of two) beyond; as
+// many CTAs per SM as
 // `sm_threads` threads are (registers), at most 16.
-Shape row_shape(int width, int elem, int arrays, int sm_threads) {
+Shape row_shape(int width, int elem, int arrays, int one, int sm_threads) {
   Shape s;
   const int bytes = (width * elem) % 16 == 0 ? 16 : (width * elem) % 4 == 0 ? 4 : 2;
   s.vec = bytes / elem;
   const int nvec = width / s.vec;
-  s.n = 1;
+  s.n = nvec <= one ? 1 : 2;
   while (s.n * kMaxThreads < nvec) s.n *= 2;
   s.threads = ((nvec + s.n - 1) / s.n + 31) / 32 * 32;
   s.per_sm = sm_threads / (s.n > 1 && sm_threads > kMaxThreads ? 2 : 1) / s.threads;
@@ -528,8 +543,10 @@ cudaError_t launch_any(const BlockNormProblem& p, const Shape& s, cudaStream_t s
   return s.vec == 4 ? launch_v<BWD, float, 4>(p, s, st) : launch_v<BWD, float, 1>(p, s, st);
 }
 
-Shape fwd_shape(int width, int elem) { return row_shape(width, elem, 3, kFwdThreads); }
-Shape bwd_shape(int width, int elem) { return row_shape(width, elem, 5, kBwdThreads); }
+// (65536 x 4096 bf16 forward: 475 us with 256 threads of two pieces, 501 with 512
+// of one; 16384 x 4096 backward, whose sums double the registers: 270 and 233.)
+Shape fwd_shape(int width, int elem) { return row_shape(width, elem, 3, 256, kFwdThreads); }
+Shape bwd_shape(int width, int elem) { return row_shape(width, elem, 5, kMaxThreads, kBwdThreads); }
 
 }  // namespace
 
@@ -549,7 +566,8 @@ cudaError_t launch_block_norm_backward(const BlockNormProblem& p, cudaStream_t s
   const Shape s = bwd_shape(p.width, p.bf16 ? 2 : 4);
   const cudaError_t e = launch_any<true>(p, s, st);
   if (e != cudaSuccess || !(p.w_next || p.scale || p.w_post)) return e;
-  return launch_pdl(true, block_norm_reduce_kernel, dim3((p.width + 31) / 32, 2), dim3(32, 32), 0, st, p,
+  return launch_pdl(true, block_norm_reduce_kernel, dim3((p.width + kSumCols - 1) / kSumCols, 2),
+                    dim3(kSumCols, kSumRows), 0, st, p,
                     row_grid(p.rows, s));
 }
 
