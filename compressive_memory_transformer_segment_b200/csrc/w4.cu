@@ -21,8 +21,9 @@
 // same 8 channels of a token are 16 contiguous bytes.  So both operands go
 // from global memory to the tensor cores without shared memory or shuffles.
 //
-// A CTA takes 16 rows; its 8 warps share out the row's blocks, and their sums
-// are added in warp order through shared memory.
+// A CTA takes 16 rows, or 64 where that still fills the GPU (a token's channels
+// are then read once for four tiles of rows); its 8 warps share out the rows'
+// blocks, and their sums are added in warp order through shared memory.
 #include "common.cuh"
 #include "kernels.h"
 #include "q4_common.cuh"
@@ -34,28 +35,46 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kBlock = 128;  // channels of a packed block
-constexpr int kTile = 16;    // rows of a CTA
+constexpr int kTile = 16;    // rows of a tile
+constexpr int kSMs = 148;
+#ifndef WS
+#define WS kSMs
+#endif
 
-// Scale (fp32) and bias pair (bf16x2 of 128 + zero) of a row's groups in one
-// block; NG groups of 128 / NG channels.
+// Scales and zeros of a row's NG groups (of 128 / NG channels) in one block, as
+// they lie in memory.
 template <int NG>
 struct GroupParams {
-  __nv_bfloat16 s[NG];
-  uint8_t z[NG];
-  // Groups from `groups` on hold no channel below K; their scale is taken as
-  // 0, whatever the array holds there.
-  __device__ __forceinline__ void load(const __nv_bfloat16* scales, const uint8_t* zeros, size_t row,
-                                       int per_row, int blk, int groups) {
-#pragma unroll
-    for (int i = 0; i < NG; ++i) {
-      const int at = blk * NG + i;
-      const bool in = at < groups;
-      s[i] = in ? scales[row * per_row + at] : __float2bfloat16_rn(0.f);
-      z[i] = in && zeros ? zeros[row * per_row + at] : (uint8_t)8;
+  uint32_t s[NG == 4 ? 2 : 1];  // bf16
+  uint32_t z;                   // bytes
+  __device__ __forceinline__ void load(const __nv_bfloat16* scales, const uint8_t* zeros) {
+    z = 0x08080808u;
+    if constexpr (NG == 4) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(scales));
+      s[0] = v.x; s[1] = v.y;
+      if (zeros) z = __ldg(reinterpret_cast<const uint32_t*>(zeros));
+    } else if constexpr (NG == 2) {
+      s[0] = __ldg(reinterpret_cast<const uint32_t*>(scales));
+      if (zeros) z = __ldg(reinterpret_cast<const unsigned short*>(zeros));
+    } else {
+      s[0] = __ldg(reinterpret_cast<const unsigned short*>(scales));
+      if (zeros) z = __ldg(zeros);
     }
   }
-  __device__ __forceinline__ float scale(int i) const { return __bfloat162float(s[i]); }
-  __device__ __forceinline__ uint32_t bias(int i) const { return kCodeBias2 + z[i] * 0x00010001u; }
+  // The scales of groups without a channel below K count as 0, whatever the
+  // array holds there: only `groups` (at least one) of the block's do.
+  __device__ __forceinline__ void cut(int groups) {
+#pragma unroll
+    for (int g = 1; g < NG; ++g)
+      if (g >= groups) s[g >> 1] &= g & 1 ? 0x0000ffffu : 0xffff0000u;
+  }
+  __device__ __forceinline__ float scale(int g) const {
+    return __uint_as_float(g & 1 ? s[g >> 1] & 0xffff0000u : s[g >> 1] << 16);
+  }
+  // bf16x2 of 128 + zero.
+  __device__ __forceinline__ uint32_t bias(int g) const {
+    return kCodeBias2 + __byte_perm(z, 0, 0x4040 + g * 0x0101);
+  }
 };
 
 // 8 channels of a token as B fragments: parts of 4 bf16 pairs.
@@ -64,7 +83,7 @@ template <> struct TokenFrag<__nv_bfloat16> {
   static constexpr int kParts = 1;
   uint32_t b[1][4];
   __device__ __forceinline__ void load(const __nv_bfloat16* x, bool in) {
-    const uint4 v = in ? __ldg(reinterpret_cast<const uint4*>(x)) : uint4{0, 0, 0, 0};
+    const uint4 v = in ? *reinterpret_cast<const uint4*>(x) : uint4{0, 0, 0, 0};
     b[0][0] = v.x; b[0][1] = v.y; b[0][2] = v.z; b[0][3] = v.w;
   }
 };
@@ -72,11 +91,14 @@ template <> struct TokenFrag<float> {
   static constexpr int kParts = 3;
   uint32_t b[3][4];
   __device__ __forceinline__ void load(const float* x, bool in) {
-    float4 v[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+    float4 v[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
     if (in) {
-      v[0] = __ldg(reinterpret_cast<const float4*>(x));
-      v[1] = __ldg(reinterpret_cast<const float4*>(x) + 1);
+      v[0] = *reinterpret_cast<const float4*>(x);
+      v[1] = reinterpret_cast<const float4*>(x)[1];
     }
+    set(v);
+  }
+  __device__ __forceinline__ void set(float4 (&v)[2]) {
 #pragma unroll
     for (int part = 0; part < 3; ++part) {
       b[part][0] = split_bf16(v[0].x, v[0].y);
@@ -91,83 +113,201 @@ template <> struct TokenFrag<float> {
 // 16 consecutive rows; a projection into heads takes rows i0 .. i0 + 7 of one
 // head and their partners i + d/2, so that one lane holds both halves of a
 // rotation.
-template <bool QKV>
 __device__ __forceinline__ int tile_row(const W4Problem& p, int tile, int m) {
-  if constexpr (!QKV) return tile * kTile + m;
+  if (p.q == nullptr) return tile * kTile + m;
   const int per_head = p.d / kTile;
   const int head = tile / per_head, i0 = (tile - head * per_head) * 8;
   return head * p.d + i0 + (m < 8 ? m : m - 8 + p.d / 2);
 }
 
-template <typename T, int NT, int NG, bool QKV>
-__global__ void __launch_bounds__(kThreads)
-w4_kernel(W4Problem p) {
-  constexpr int kTok = NT * 8;
-  constexpr int kParts = TokenFrag<T>::kParts;
+// A row tile's codes of a block (rows a and b of this lane) times NT token tiles,
+// into acc; piece(j, f): the tokens' fragments of channels 32 j ...
+template <typename T, int NT, int NG, typename F>
+__device__ __forceinline__ void multiply(const uint4& a, const uint4& b, const GroupParams<NG>& pa,
+                                         const GroupParams<NG>& pb, F&& piece, float (&acc)[NT][4]) {
+  const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
+  float s[NT][4];
+  uint32_t ba = 0, bb = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int g = j * NG / 4;
+    const bool first = j % (4 / NG) == 0, last = (j + 1) % (4 / NG) == 0;
+    if (first) {
+      ba = pa.bias(g);
+      bb = pb.bias(g);
+    }
+    uint32_t fa[4], fb[4];
+    unpack_codes(wa[j], ba, fa);
+    unpack_codes(wb[j], bb, fb);
+    TokenFrag<T> f[NT];
+    piece(j, f);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      if (first)
+        mma_bf16_first(s[n], fa[0], fb[0], fa[1], fb[1], f[n].b[0][0], f[n].b[0][1]);
+      else
+        mma_bf16(s[n], fa[0], fb[0], fa[1], fb[1], f[n].b[0][0], f[n].b[0][1]);
+      mma_bf16(s[n], fa[2], fb[2], fa[3], fb[3], f[n].b[0][2], f[n].b[0][3]);
+#pragma unroll
+      for (int part = 1; part < TokenFrag<T>::kParts; ++part) {
+        mma_bf16(s[n], fa[0], fb[0], fa[1], fb[1], f[n].b[part][0], f[n].b[part][1]);
+        mma_bf16(s[n], fa[2], fb[2], fa[3], fb[3], f[n].b[part][2], f[n].b[part][3]);
+      }
+      if (last) {
+        const float sa = pa.scale(g), sb = pb.scale(g);
+        acc[n][0] = fmaf(sa, s[n][0], acc[n][0]);
+        acc[n][1] = fmaf(sa, s[n][1], acc[n][1]);
+        acc[n][2] = fmaf(sb, s[n][2], acc[n][2]);
+        acc[n][3] = fmaf(sb, s[n][3], acc[n][3]);
+      }
+    }
+  }
+}
+
+// Where a lane's row of the weights lies.
+template <int NG>
+struct Row {
+  const uint8_t* codes;  // its 16 bytes of the first block
+  const __nv_bfloat16* scales;
+  const uint8_t* zeros;  // or null
+  __device__ __forceinline__ Row(const W4Problem& p, int tile, int m, int nblk, int c) {
+    // Rows past the last are read as the last one and never stored.
+    const size_t row = min(tile_row(p, tile, m), p.N - 1);
+    codes = p.packed + row * nblk * (kBlock / 2) + c * 16;
+    scales = p.scales + row * nblk * NG;
+    zeros = p.zeros ? p.zeros + row * nblk * NG : nullptr;
+  }
+  __device__ __forceinline__ const uint8_t* block(int blk) const { return codes + (uint32_t)blk * (kBlock / 2); }
+  __device__ __forceinline__ void load(GroupParams<NG>& to, int blk) const {
+    to.load(scales + blk * NG, zeros ? zeros + blk * NG : nullptr);
+  }
+};
+
+// A finished tile to the outputs: value(m, t) is row m's sum for token t of this
+// pass; `threads` threads, this one `thread`.
+template <typename T, typename F>
+__device__ __forceinline__ void write_tile(const W4Problem& p, int tile, int t0, int nt, int thread, int threads,
+                                           F&& value) {
+  if (p.q == nullptr) {
+    for (int at = thread; at < kTile * nt; at += threads) {
+      const int t = at / kTile, m = at % kTile, n = tile * kTile + m;
+      if (n < p.N) {
+        float y = value(m, t);
+        if (p.bias) y += p.bias[n];
+        static_cast<T*>(p.y)[(size_t)(t0 + t) * p.N + n] = from_f32<T>(y);
+      }
+    }
+    return;
+  }
+  const int half = p.d / 2, first = tile_row(p, tile, 0);
+  for (int at = thread; first < p.N && at < 8 * nt; at += threads) {
+    const int t = at / 8, m = at % 8, n = first + m;
+    const int head = n / p.d, e = n - head * p.d;
+    float y0 = value(m, t), y1 = value(m + 8, t);
+    if (p.bias) {
+      y0 += p.bias[n];
+      y1 += p.bias[n + half];
+    }
+    const int tok = t0 + t, b = tok / p.L, l = tok - b * p.L;
+    if (p.rope_cos && head < p.H_q + p.H_kv) {
+      const int pos = p.positions ? p.positions[tok] : l;
+      if (pos >= 0 && pos < p.n_pos) {
+        const float cs = p.rope_cos[(size_t)pos * half + e], sn = p.rope_sin[(size_t)pos * half + e];
+        const float r0 = y0 * cs - y1 * sn;
+        y1 = y1 * cs + y0 * sn;
+        y0 = r0;
+      } else {
+        atomicOr(p.status, kStatusRange);
+      }
+    }
+    T* out;
+    int heads, h = head;
+    if (h < p.H_q) {
+      out = static_cast<T*>(p.q); heads = p.H_q;
+    } else if (h < p.H_q + p.H_kv) {
+      out = static_cast<T*>(p.k); heads = p.H_kv; h -= p.H_q;
+    } else {
+      out = static_cast<T*>(p.v); heads = p.H_kv; h -= p.H_q + p.H_kv;
+    }
+    out += ((size_t)(b * heads + h) * p.L + l) * p.d + e;
+    out[0] = from_f32<T>(y0);
+    out[half] = from_f32<T>(y1);
+  }
+}
+
+// A CTA per tile of 16 rows, whose 8 warps share out the blocks: the most
+// parallelism for few tokens or few rows.  A warp has the codes of its next four
+// blocks on their way (all of its blocks, up to 4096 channels), copied to shared
+// memory by the lanes that will read them, so that they take no registers and
+// need no barrier.  NT: tiles of 8 tokens.
+template <typename T, int NT, int NG>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1)
+w4_split_kernel(W4Problem p) {
+  constexpr int kTok = NT * 8, kAhead = 4;
   __shared__ float red[kWarps][kTile][kTok + 1];
+  extern __shared__ __align__(16) uint8_t smem[];  // [kWarps][kAhead][2][32] pieces of 16 bytes
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int i = lane >> 2, c = lane & 3;
   const int t0 = blockIdx.y * kTok;
   const int nt = min(kTok, p.M - t0);
   const int nblk = (p.K + kBlock - 1) / kBlock;
-  const int groups = (p.K + kBlock / NG - 1) / (kBlock / NG);
-  // Rows past the last are read as the last one and never stored.
-  const size_t row_a = min(tile_row<QKV>(p, blockIdx.x, i), p.N - 1);
-  const size_t row_b = min(tile_row<QKV>(p, blockIdx.x, i + 8), p.N - 1);
-  const uint8_t* wa_p = p.packed + row_a * nblk * (kBlock / 2) + c * 16;
-  const uint8_t* wb_p = p.packed + row_b * nblk * (kBlock / 2) + c * 16;
-  const T* x = static_cast<const T*>(p.x);
-
+  const Row<NG> ra(p, blockIdx.x, i, nblk, c), rb(p, blockIdx.x, i + 8, nblk, c);
+  const T* x = static_cast<const T*>(p.x) + (size_t)(t0 + i) * p.K + 8 * c;  // this lane's first token
+  uint4* mine = reinterpret_cast<uint4*>(smem) + warp * kAhead * 64 + lane;
+  GroupParams<NG> par[kAhead][2];
+  auto start = [&](int u, int blk) {
+    if (blk < nblk) {
+      const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(mine + u * 64));
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(ra.block(blk)) : "memory");
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 512), "l"(rb.block(blk)) : "memory");
+      ra.load(par[u][0], blk);
+      rb.load(par[u][1], blk);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) start(u, warp + u * kWarps);
   float acc[NT][4];
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
-
-  uint4 na = {0, 0, 0, 0}, nb = {0, 0, 0, 0};
-  GroupParams<NG> pa, pb;
-  if (warp < nblk) {
-    na = ld_once_16(wa_p + (size_t)warp * (kBlock / 2));
-    nb = ld_once_16(wb_p + (size_t)warp * (kBlock / 2));
-    pa.load(p.scales, p.zeros, row_a, nblk * NG, warp, groups);
-    pb.load(p.scales, p.zeros, row_b, nblk * NG, warp, groups);
-  }
-  for (int blk = warp; blk < nblk; blk += kWarps) {
-    const uint32_t wa[4] = {na.x, na.y, na.z, na.w}, wb[4] = {nb.x, nb.y, nb.z, nb.w};
-    const GroupParams<NG> ga = pa, gb = pb;
-    const int next = blk + kWarps;
-    if (next < nblk) {
-      na = ld_once_16(wa_p + (size_t)next * (kBlock / 2));
-      nb = ld_once_16(wb_p + (size_t)next * (kBlock / 2));
-      pa.load(p.scales, p.zeros, row_a, nblk * NG, next, groups);
-      pb.load(p.scales, p.zeros, row_b, nblk * NG, next, groups);
-    }
-    float sum[NT][4];
+  // bf16 tokens of a block are loaded together, fp32 ones (twice the registers,
+  // and three parts) piece by piece.
+  constexpr bool kTogether = TokenFrag<T>::kParts == 1 && NT <= 2;
+#pragma unroll 1
+  for (int b0 = warp; b0 < nblk; b0 += kWarps * kAhead) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int g = j * NG / 4;
-      uint32_t fa[4], fb[4];
-      unpack_codes(wa[j], ga.bias(g), fa);
-      unpack_codes(wb[j], gb.bias(g), fb);
-      const bool first = j % (4 / NG) == 0, last = (j + 1) % (4 / NG) == 0;
-      const int k0 = blk * kBlock + 32 * j + 8 * c;
+    for (int u = 0; u < kAhead; ++u) {
+      const int blk = b0 + u * kWarps;
+      if (blk < nblk) {
+        const T* xb = x + (uint32_t)blk * kBlock;
+        const int left = p.K - blk * kBlock - 8 * c;  // channels from this lane's on
+        auto tokens = [&](int j, TokenFrag<T>(&to)[NT]) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        if (first) sum[n][0] = sum[n][1] = sum[n][2] = sum[n][3] = 0.f;
-        const int t = n * 8 + i;
-        TokenFrag<T> f;
-        f.load(x + (size_t)(t0 + t) * p.K + k0, t < nt && k0 < p.K);
+          for (int n = 0; n < NT; ++n) to[n].load(xb + (size_t)(n * 8) * p.K + 32 * j, n * 8 + i < nt && 32 * j < left);
+        };
+        TokenFrag<T> f[kTogether ? 4 : 1][NT];
+        if constexpr (kTogether) {
 #pragma unroll
-        for (int part = 0; part < kParts; ++part) {
-          mma_bf16(sum[n], fa[0], fb[0], fa[1], fb[1], f.b[part][0], f.b[part][1]);
-          mma_bf16(sum[n], fa[2], fb[2], fa[3], fb[3], f.b[part][2], f.b[part][3]);
+          for (int j = 0; j < 4; ++j) tokens(j, f[j]);
         }
-        if (last) {
-          acc[n][0] = fmaf(ga.scale(g), sum[n][0], acc[n][0]);
-          acc[n][1] = fmaf(ga.scale(g), sum[n][1], acc[n][1]);
-          acc[n][2] = fmaf(gb.scale(g), sum[n][2], acc[n][2]);
-          acc[n][3] = fmaf(gb.scale(g), sum[n][3], acc[n][3]);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+        const uint4 ca = mine[u * 64], cb = mine[u * 64 + 32];
+        if (NG > 1 && blk == nblk - 1) {
+          const int groups = (p.K - blk * kBlock + kBlock / NG - 1) / (kBlock / NG);
+          par[u][0].cut(groups);
+          par[u][1].cut(groups);
         }
+        multiply<T, NT, NG>(ca, cb, par[u][0], par[u][1], [&](int j, TokenFrag<T>(&to)[NT]) {
+          if constexpr (kTogether) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) to[n] = f[j][n];
+          } else {
+            tokens(j, to);
+          }
+        }, acc);
+        start(u, blk + kWarps * kAhead);
       }
     }
   }
@@ -179,83 +319,159 @@ w4_kernel(W4Problem p) {
     red[warp][i + 8][n * 8 + 2 * c + 1] = acc[n][3];
   }
   __syncthreads();
-  auto total = [&](int m, int t) {
+  write_tile<T>(p, blockIdx.x, t0, nt, threadIdx.x, kThreads, [&](int m, int t) {
     float s = red[0][m][t];
 #pragma unroll
     for (int w = 1; w < kWarps; ++w) s += red[w][m][t];
     return s;
-  };
-  if constexpr (!QKV) {
-    for (int at = threadIdx.x; at < kTile * nt; at += kThreads) {
-      const int t = at / kTile, m = at % kTile;
-      const int row = blockIdx.x * kTile + m;
-      if (row < p.N) {
-        float y = total(m, t);
-        if (p.bias) y += p.bias[row];
-        static_cast<T*>(p.y)[(size_t)(t0 + t) * p.N + row] = from_f32<T>(y);
-      }
-    }
-  } else {
-    const int half = p.d / 2;
-    for (int at = threadIdx.x; at < 8 * nt; at += kThreads) {
-      const int t = at / 8, m = at % 8;
-      const int row = tile_row<true>(p, blockIdx.x, m);
-      const int head = row / p.d, e = row - head * p.d;
-      float y0 = total(m, t), y1 = total(m + 8, t);
-      if (p.bias) {
-        y0 += p.bias[row];
-        y1 += p.bias[row + half];
-      }
-      const int tok = t0 + t, b = tok / p.L, l = tok - b * p.L;
-      if (p.rope_cos && head < p.H_q + p.H_kv) {
-        const int pos = p.positions ? p.positions[tok] : l;
-        if (pos >= 0 && pos < p.n_pos) {
-          const float cs = p.rope_cos[(size_t)pos * half + e], sn = p.rope_sin[(size_t)pos * half + e];
-          const float r0 = y0 * cs - y1 * sn;
-          y1 = y1 * cs + y0 * sn;
-          y0 = r0;
-        } else {
-          atomicOr(p.status, kStatusRange);
-        }
-      }
-      T* out;
-      int heads, h = head;
-      if (h < p.H_q) {
-        out = static_cast<T*>(p.q); heads = p.H_q;
-      } else if (h < p.H_q + p.H_kv) {
-        out = static_cast<T*>(p.k); heads = p.H_kv; h -= p.H_q;
-      } else {
-        out = static_cast<T*>(p.v); heads = p.H_kv; h -= p.H_q + p.H_kv;
-      }
-      out += ((size_t)(b * heads + h) * p.L + l) * p.d + e;
-      out[0] = from_f32<T>(y0);
-      out[half] = from_f32<T>(y1);
-    }
-  }
+  });
 }
 
-template <typename T, int NG, bool QKV>
+// A CTA per 64 rows, one tile a warp, all blocks in turn: the tokens' channels of
+// a block are copied to shared memory once for the four tiles, two blocks ahead,
+// and a warp's codes are loaded three blocks ahead into registers.
+constexpr int kRowWarps = 4;
+
+template <typename T, int NT, int NG>
+__global__ void __launch_bounds__(kRowWarps * 32, NT <= 2 ? 4 : NT == 4 ? 3 : 2)
+w4_rows_kernel(W4Problem p) {
+  constexpr int kTok = NT * 8, kStages = 4;
+  constexpr int kRowBytes = kBlock * (int)sizeof(T), kPieces = kRowBytes / 16;  // of a token and block
+  extern __shared__ __align__(16) uint8_t smem[];                               // [kStages][kTok][kRowBytes]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int i = lane >> 2, c = lane & 3;
+  const int t0 = blockIdx.y * kTok;
+  const int nt = min(kTok, p.M - t0);
+  const int nblk = (p.K + kBlock - 1) / kBlock;
+  const int tile = blockIdx.x * kRowWarps + warp;
+  const Row<NG> ra(p, tile, i, nblk, c), rb(p, tile, i + 8, nblk, c);
+  const uint8_t* x = reinterpret_cast<const uint8_t*>(static_cast<const T*>(p.x) + (size_t)t0 * p.K);
+  // Piece q of token t lies at q ^ swizzle(t): the 8 lanes that read together
+  // (two tokens, 4 or 8 pieces apart) then reach different banks.
+  auto swizzle = [](int t) { return sizeof(T) == 2 ? (t & 1) * 4 : 0; };
+  auto copy = [&](int blk) {
+    if (blk < nblk) {
+      uint8_t* stage = smem + (blk % kStages) * (kTok * kRowBytes);
+      const int left = (p.K - blk * kBlock) * (int)sizeof(T);  // bytes of a row from here
+#pragma unroll
+      for (int e = threadIdx.x; e < kTok * kPieces; e += kRowWarps * 32) {
+        const int t = e / kPieces, q = e % kPieces;
+        uint8_t* dst = stage + t * kRowBytes + (q ^ swizzle(t)) * 16;
+        if (t < nt && q * 16 < left) {
+          const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to),
+                       "l"(x + ((size_t)t * p.K + blk * kBlock) * sizeof(T) + q * 16) : "memory");
+        } else {
+          *reinterpret_cast<uint4*>(dst) = uint4{0, 0, 0, 0};
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  float acc[NT][4];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
+  struct Block {
+    uint4 a, b;
+    GroupParams<NG> pa, pb;
+  } w[3];
+  auto load = [&](Block& to, int blk) {
+    if (blk < nblk) {
+      to.a = ld_once_16(ra.block(blk));
+      to.b = ld_once_16(rb.block(blk));
+      ra.load(to.pa, blk);
+      rb.load(to.pb, blk);
+    }
+  };
+#pragma unroll
+  for (int e = 0; e < 3; ++e) load(w[e], e);
+#pragma unroll
+  for (int e = 0; e < kStages - 2; ++e) copy(e);
+  auto use = [&](Block& r, int blk) {
+    copy(blk + kStages - 2);  // (its slot was last read two blocks ago, before the last barrier)
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    __syncthreads();
+    const uint8_t* stage = smem + (blk % kStages) * (kTok * kRowBytes);
+    if (NG > 1 && blk == nblk - 1) {
+      const int groups = (p.K - blk * kBlock + kBlock / NG - 1) / (kBlock / NG);
+      r.pa.cut(groups);
+      r.pb.cut(groups);
+    }
+    multiply<T, NT, NG>(r.a, r.b, r.pa, r.pb, [&](int j, TokenFrag<T>(&to)[NT]) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const int t = n * 8 + i;
+        const int q = (sizeof(T) == 2 ? 4 * j + c : 8 * j + 2 * c) ^ swizzle(t);
+        to[n].load(reinterpret_cast<const T*>(stage + t * kRowBytes + q * 16), true);
+      }
+    }, acc);
+    load(r, blk + 3);
+  };
+#pragma unroll 1
+  for (int blk = 0; blk < nblk; blk += 3) {
+    use(w[0], blk);
+    if (blk + 1 < nblk) use(w[1], blk + 1);
+    if (blk + 2 < nblk) use(w[2], blk + 2);
+  }
+  // Each warp's sums to its own part of shared memory, in order of rows.
+  __syncthreads();
+  float(*mine)[kTok + 1] = reinterpret_cast<float(*)[kTok + 1]>(smem) + warp * kTile;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    mine[i][n * 8 + 2 * c] = acc[n][0];
+    mine[i][n * 8 + 2 * c + 1] = acc[n][1];
+    mine[i + 8][n * 8 + 2 * c] = acc[n][2];
+    mine[i + 8][n * 8 + 2 * c + 1] = acc[n][3];
+  }
+  __syncwarp();
+  write_tile<T>(p, tile, t0, nt, lane, 32, [&](int m, int t) { return mine[m][t]; });
+}
+
+template <typename T, int NT, int NG>
 cudaError_t launch_tokens(const W4Problem& p, cudaStream_t st) {
-  const unsigned tiles = (p.N + kTile - 1) / kTile;
-  // 8, 16, 32 or 64 tokens a pass: the least that holds them all.
-  if (p.M <= 8)
-    w4_kernel<T, 1, NG, QKV><<<dim3(tiles, 1), kThreads, 0, st>>>(p);
-  else if (p.M <= 16)
-    w4_kernel<T, 2, NG, QKV><<<dim3(tiles, 1), kThreads, 0, st>>>(p);
-  else if (p.M <= 32)
-    w4_kernel<T, 4, NG, QKV><<<dim3(tiles, 1), kThreads, 0, st>>>(p);
-  else
-    w4_kernel<T, 8, NG, QKV><<<dim3(tiles, (p.M + 63) / 64), kThreads, 0, st>>>(p);
+  const unsigned tiles = (p.N + kTile - 1) / kTile, passes = (p.M + NT * 8 - 1) / (NT * 8);
+  // 64 rows a CTA where that gives every SM one: 16 tokens, 4096 -> 16384 take
+  // WIDE_ROWS us so and WIDE_SPLIT us with the blocks shared out.  With 8 tokens or
+  // fewer there is little to share, and the split is as fast or faster.
+  if constexpr (NT > 1) {
+    if (tiles >= (unsigned)(kRowWarps * WS)) {
+      constexpr int copies = 4 * NT * 8 * kBlock * (int)sizeof(T), sums = kRowWarps * kTile * (NT * 8 + 1) * 4;
+      constexpr int bytes = copies > sums ? copies : sums;
+      if (bytes > 48 * 1024) {
+        cudaError_t e =
+            cudaFuncSetAttribute(w4_rows_kernel<T, NT, NG>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) return e;
+      }
+      w4_rows_kernel<T, NT, NG><<<dim3((tiles + kRowWarps - 1) / kRowWarps, passes), kRowWarps * 32, bytes, st>>>(p);
+      return cudaGetLastError();
+    }
+  }
+  constexpr int ring = kWarps * 4 * 64 * 16, fixed = kWarps * kTile * (NT * 8 + 1) * 4;
+  if (ring + fixed > 48 * 1024) {
+    cudaError_t e = cudaFuncSetAttribute(w4_split_kernel<T, NT, NG>, cudaFuncAttributeMaxDynamicSharedMemorySize, ring);
+    if (e != cudaSuccess) return e;
+  }
+  w4_split_kernel<T, NT, NG><<<dim3(tiles, passes), kThreads, ring, st>>>(p);
   return cudaGetLastError();
+}
+
+// 8, 16, 32 or 64 tokens a pass: the least that holds them all.
+template <typename T, int NG>
+cudaError_t launch_group(const W4Problem& p, cudaStream_t st) {
+  if (p.M <= 8) return launch_tokens<T, 1, NG>(p, st);
+  if (p.M <= 16) return launch_tokens<T, 2, NG>(p, st);
+  if (p.M <= 32) return launch_tokens<T, 4, NG>(p, st);
+  return launch_tokens<T, 8, NG>(p, st);
 }
 
 template <typename T>
 cudaError_t launch_type(const W4Problem& p, cudaStream_t st) {
-  const bool qkv = p.q != nullptr;
   switch (p.group) {
-    case 32: return qkv ? launch_tokens<T, 4, true>(p, st) : launch_tokens<T, 4, false>(p, st);
-    case 64: return qkv ? launch_tokens<T, 2, true>(p, st) : launch_tokens<T, 2, false>(p, st);
-    case 128: return qkv ? launch_tokens<T, 1, true>(p, st) : launch_tokens<T, 1, false>(p, st);
+    case 32: return launch_group<T, 4>(p, st);
+    case 64: return launch_group<T, 2>(p, st);
+    case 128: return launch_group<T, 1>(p, st);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -381,7 +597,7 @@ cudaError_t launch_w4_layout(const W4PackProblem& p, W4Layout what, cudaStream_t
       break;
     case W4Layout::kPack: w4_pack_kernel<<<grid, kThreads, 0, st>>>(p); break;
     case W4Layout::kDequantize: {
-      const unsigned g = grid < 148u * 16u ? grid : 148u * 16u;
+      const unsigned g = grid < kSMs * 16u ? grid : kSMs * 16u;
       if (p.bf16) w4_dequantize_kernel<__nv_bfloat16><<<g, kThreads, 0, st>>>(p);
       else w4_dequantize_kernel<float><<<g, kThreads, 0, st>>>(p);
       break;
