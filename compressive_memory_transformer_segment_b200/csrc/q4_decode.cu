@@ -41,7 +41,8 @@ namespace infini {
 
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 128;       // of a CTA that attends
+constexpr int kMoveThreads = 256;   // of one that appends or reads rows
 constexpr int kWarps = kThreads / 32;
 constexpr int kHeads = 8;               // query heads of a CTA (columns of a product)
 constexpr int kUnit = kWarps * 32;      // rows of the smallest share of the work
@@ -95,6 +96,11 @@ __device__ __forceinline__ float column_max(float x) {
   return x;
 }
 
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(b));
+  return a;
+}
+
 // 8 channels 8 w .. 8 w + 7 of a row, held by one lane, into the buffer; the 4
 // lanes of a 32-channel group are neighbours and call together.  fp32
 // arithmetic with one rounding per operation; a group with a NaN becomes NaN.
@@ -103,64 +109,64 @@ __device__ __forceinline__ void store_group(const float (&x)[8], int w, bool key
                                             __nv_bfloat16* sm, bool active) {
   constexpr int NJ = D / 32;
   const int j = w >> 2, c = w & 3;
-  float lo = x[0], hi = x[0];
-  int nan = x[0] != x[0];
+  float lo = x[0], hi = x[0];  // hi is NaN once a value is
 #pragma unroll
   for (int e = 1; e < 8; ++e) {
     lo = fminf(lo, x[e]);
-    hi = fmaxf(hi, x[e]);
-    nan |= x[e] != x[e];
+    hi = max_or_nan(hi, x[e]);
   }
 #pragma unroll
   for (int o = 1; o < 4; o <<= 1) {
     lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-    nan |= __shfl_xor_sync(0xffffffffu, nan, o);
+    hi = max_or_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
   }
   __nv_bfloat162 par;
   par.y = __float2bfloat16_rn(lo);
   const float m = __bfloat162float(par.y);
   par.x = __float2bfloat16_rn(__fmul_rn(fmaxf(__fsub_rn(hi, m), 0.f), 1.f / 15.f));
   const float s = __bfloat162float(par.x);
-  if (nan) par = __floats2bfloat162_rn(NAN, NAN);
-  // Codes: the rounded quotient (x - m) / s, to the nearest integer.  A product
-  // with the reciprocal decides it unless it lies within 2^-10 of a half, where
-  // the division itself does (rarely, so the eight divisions' code is one loop).
-  const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
+  if (hi != hi) par = __floats2bfloat162_rn(NAN, NAN);
+  // Codes: the quotient (x - m) / s rounded to the nearest integer, ties to even,
+  // in 0..15.  An approximate quotient finds the half h = k + 1/2 nearest to it; the
+  // sign of x - m - h s, which one fused operation gives exactly (h s fits 13 bits),
+  // then says on which side of h the quotient lies.  Rounding the quotient to fp32
+  // first changes nothing: where x - m is not h s it differs by 2^-24 of it or
+  // more, and half a step at h is less.  Ties are not rare (bf16 values and a bf16
+  // scale: about one group in eight has one), so no branch looks for them.
+  float d[8], s1 = s;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) d[e] = __fsub_rn(x[e], m);
+  if (!(s >= 0x1p-100f && s < INFINITY)) {  // all codes 0, or a scale whose reciprocal overflows
+    const bool none = !(s > 0.f && s < INFINITY);
+    s1 = none ? 1.f : s * 0x1p100f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) d[e] = none ? 0.f : d[e] * 0x1p100f;
+  }
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s1));
+  inv *= 1.f / 14.f;
+  constexpr float kRound = 12582912.f;  // 1.5 2^23: a sum with it has an integer in its low bits
   uint32_t q[8];
-  uint32_t close = 0;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const float t = __fsub_rn(x[e], m) * inv, n = rintf(t);
-    if (!(fabsf(t - n) < 0.499f) && inv > 0.f) close |= 1u << e;
-    q[e] = (uint32_t)fminf(fmaxf(n, 0.f), 15.f);
-  }
-  if (close) {
-#pragma unroll 1
-    for (int e = 0; e < 8; ++e) {
-      if (!(close >> e & 1)) continue;
-      float v = x[0];
-#pragma unroll
-      for (int k = 1; k < 8; ++k) v = k == e ? x[k] : v;
-      const float n = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(v, m), s)), 0.f), 15.f);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) q[k] = k == e ? (uint32_t)n : q[k];
-    }
+    const float u = fmaf(__saturatef(fmaf(d[e], inv, -0.5f / 14.f)), 14.f, kRound);
+    const float r = fmaf(-__fadd_rn(__fsub_rn(u, kRound), 0.5f), s1, d[e]);
+    q[e] = __float_as_uint(u) & 15u;
+    q[e] += __float_as_int(r) + (int)(q[e] & 1u) > 0;  // r > 0, or 0 and k odd
   }
   if (!active) return;
+  uint32_t word = 0;
   if (key) {
-    uint32_t word = 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) word |= q[e] << ((e & 1) ? 2 * e + 14 : 2 * e);
+    for (int e = 0; e < 8; ++e)
+      word += q[e] << ((e & 1) ? 2 * e + 14 : 2 * e);
     reinterpret_cast<uint32_t*>(codes)[c * NJ + j] = word;
   } else {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      uint32_t half = 0;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) half |= q[4 * u + e] << (4 * e);
-      reinterpret_cast<unsigned short*>(codes)[(2 * c + u) * NJ + j] = (unsigned short)half;
-    }
+    for (int e = 0; e < 8; ++e) word += q[e] << 4 * e;
+    unsigned short* halves = reinterpret_cast<unsigned short*>(codes);
+    halves[2 * c * NJ + j] = (unsigned short)word;
+    halves[(2 * c + 1) * NJ + j] = (unsigned short)(word >> 16);
   }
   if (c == 0) reinterpret_cast<__nv_bfloat162*>(sm)[j] = par;
 }
@@ -1081,54 +1087,87 @@ q4_decode_kernel(Q4Problem p) {
 }
 
 // Rows of k and v [B, H_kv, n, D] into the buffers from row pos[b] on.  A
-// thread takes 8 channels (16 bytes of bf16): 4 neighbours hold a group and
-// agree on its range by two exchanges, and each has whole words of the layout.
+// thread takes 8 channels (16 bytes of bf16) of kPerThread rows: 4 neighbours hold
+// a group and agree on its range by two exchanges, and each has whole words of
+// the layout.
+constexpr int kPerThread = 4;
+
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) q4_append_kernel(Q4Problem p, int n) {
-  constexpr int PR = D / 8;  // threads per row
+__global__ void __launch_bounds__(kMoveThreads) q4_append_kernel(Q4Problem p, int n) {
+  const bool key = blockIdx.z == 0;
+  constexpr int PR = D / 8, kStep = kMoveThreads / PR;  // threads per row, rows at a time
   const int bh = blockIdx.y;
   const int pos = p.pos[bh / p.H_kv];
   if (pos < 0 || pos > p.S - n) {
     if (pos != -1 && threadIdx.x == 0) atomicOr(p.status, kStatusRange);
     return;
   }
-  const unsigned t = blockIdx.x * (kThreads / PR) + threadIdx.x / PR, w = threadIdx.x % PR;
-  const bool active = t < (unsigned)n;
-  const bool key = blockIdx.z == 0;
-  const T* src = static_cast<const T*>(key ? p.k_t : p.v_t) + ((size_t)bh * n + t) * D + 8 * w;
-  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (active) load8(src, v);
-  const size_t row = (size_t)bh * p.S + pos + t;
-  store_group<D>(v, w, key, (key ? p.k_codes : p.v_codes) + row * (D / 2),
-                 (key ? p.k_scale : p.v_scale) + row * (D / 16), active);
+  const int t0 = blockIdx.x * (kStep * kPerThread) + threadIdx.x / PR, w = threadIdx.x % PR;
+  const T* src = static_cast<const T*>(key ? p.k_t : p.v_t) + ((size_t)bh * n + t0) * D + 8 * w;
+  const size_t row = (size_t)bh * p.S + pos + t0;
+  uint8_t* codes = (key ? p.k_codes : p.v_codes) + row * (D / 2);
+  __nv_bfloat16* sm = (key ? p.k_scale : p.v_scale) + row * (D / 16);
+  float v[kPerThread][8];
+#pragma unroll
+  for (int e = 0; e < kPerThread; ++e) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[e][k] = 0.f;
+    if (t0 + e * kStep < n) load8(src + e * (kStep * D), v[e]);
+  }
+#pragma unroll
+  for (int e = 0; e < kPerThread; ++e)
+    store_group<D>(v[e], w, key, codes + e * (kStep * D / 2), sm + e * (kStep * D / 16),
+                   t0 + e * kStep < n);
 }
 
 // The values of rows 0..n-1 as k and v [B, H_kv, n, D]: a thread writes 8
-// channels (one key word, two value halfwords).
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) q4_read_kernel(Q4Problem p, int n, T* k, T* v) {
-  constexpr int NJ = D / 32, PR = D / 8;
-  const int bh = blockIdx.y;
-  const bool key = blockIdx.z == 0;
-  const unsigned t = blockIdx.x * (kThreads / PR) + threadIdx.x / PR, w = threadIdx.x % PR;
-  if (t >= (unsigned)n) return;
-  const size_t row = (size_t)bh * p.S + t;
+// channels (one key word, two value halfwords) of kPerThread rows.
+template <typename T, int D, bool KEY>
+__device__ __forceinline__ void read_rows(const uint8_t* codes, const __nv_bfloat16* sm, int w,
+                                          int left, T* to) {
+  constexpr int NJ = D / 32, kStep = kMoveThreads / (D / 8);
   const int j = w >> 2, c = w & 3;
-  const __nv_bfloat162 par =
-      reinterpret_cast<const __nv_bfloat162*>((key ? p.k_scale : p.v_scale) + row * (D / 16))[j];
-  const float s = __low2float(par), m = __high2float(par);
-  float out[8];
-  if (key) {
-    const uint32_t word = reinterpret_cast<const uint32_t*>(p.k_codes + row * (D / 2))[c * NJ + j];
+  uint32_t word[kPerThread], par[kPerThread];
 #pragma unroll
-    for (int o = 0; o < 8; ++o) out[o] = fmaf(s, (float)((word >> ((o & 1) ? 2 * o + 14 : 2 * o)) & 15u), m);
-  } else {
-    const unsigned short* halves = reinterpret_cast<const unsigned short*>(p.v_codes + row * (D / 2));
-    const uint32_t pair = halves[2 * c * NJ + j] | (uint32_t)halves[(2 * c + 1) * NJ + j] << 16;
-#pragma unroll
-    for (int o = 0; o < 8; ++o) out[o] = fmaf(s, (float)((pair >> (4 * o)) & 15u), m);
+  for (int e = 0; e < kPerThread; ++e) {
+    word[e] = par[e] = 0;
+    if (e * kStep < left) {
+      par[e] = reinterpret_cast<const uint32_t*>(sm + e * (kStep * D / 16))[j];
+      if (KEY) {
+        word[e] = reinterpret_cast<const uint32_t*>(codes + e * (kStep * D / 2))[c * NJ + j];
+      } else {
+        const unsigned short* halves =
+            reinterpret_cast<const unsigned short*>(codes + e * (kStep * D / 2)) + 2 * c * NJ + j;
+        word[e] = halves[0] | (uint32_t)halves[NJ] << 16;
+      }
+    }
   }
-  store8((key ? k : v) + ((size_t)bh * n + t) * D + 8 * w, out);
+#pragma unroll
+  for (int e = 0; e < kPerThread; ++e) {
+    const float s = __uint_as_float(par[e] << 16), m = __uint_as_float(par[e] & 0xffff0000u);
+    float out[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {  // the codes from the lowest bits on: 2^23 + 16^(i % 4) code, less 2^23
+      constexpr float kBase = 8388608.f;
+      const uint32_t bits = (i < 4 ? word[e] : word[e] >> 16) & (15u << 4 * (i & 3));
+      const float at = 1.f / (1 << 4 * (i & 3));
+      const float q = fmaf(__uint_as_float(bits | 0x4b000000u), at, -kBase * at);
+      out[KEY ? (i < 4 ? 2 * i : 2 * i - 7) : i] = fmaf(s, q, m);
+    }
+    if (e * kStep < left) store8(to + e * (kStep * D), out);
+  }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kMoveThreads) q4_read_kernel(Q4Problem p, int n, T* k, T* v) {
+  constexpr int PR = D / 8, kStep = kMoveThreads / PR;
+  const int bh = blockIdx.y;
+  const int t0 = blockIdx.x * (kStep * kPerThread) + threadIdx.x / PR, w = threadIdx.x % PR;
+  const size_t row = (size_t)bh * p.S + t0, at = ((size_t)bh * n + t0) * D + 8 * w;
+  if (blockIdx.z == 0)
+    read_rows<T, D, true>(p.k_codes + row * (D / 2), p.k_scale + row * (D / 16), w, n - t0, k + at);
+  else
+    read_rows<T, D, false>(p.v_codes + row * (D / 2), p.v_scale + row * (D / 16), w, n - t0, v + at);
 }
 
 int chunks_of(int g) { return (g + kHeads - 1) / kHeads; }
@@ -1151,7 +1190,8 @@ Q4Plan q4_plan(int B, int H_q, int H_kv, int S) {
 
 template <typename T, int D>
 cudaError_t launch(const Q4Problem& p, Q4What what, int n, void* k, void* v, cudaStream_t st) {
-  const dim3 rows((unsigned)(((long long)n * (D / 8) + kThreads - 1) / kThreads), p.B * p.H_kv, 2);
+  constexpr int kRowsPerCta = kMoveThreads / (D / 8) * kPerThread;
+  const dim3 rows((unsigned)(((long long)n + kRowsPerCta - 1) / kRowsPerCta), p.B * p.H_kv, 2);
   switch (what) {
     case Q4What::kStep: {
       constexpr int bytes = kSmemBytes<D>;
@@ -1168,9 +1208,9 @@ cudaError_t launch(const Q4Problem& p, Q4What what, int n, void* k, void* v, cud
       q4_decode_kernel<T, D><<<(unsigned)plan.ctas, kThreads, bytes, st>>>(q);
       break;
     }
-    case Q4What::kAppend: q4_append_kernel<T, D><<<rows, kThreads, 0, st>>>(p, n); break;
+    case Q4What::kAppend: q4_append_kernel<T, D><<<rows, kMoveThreads, 0, st>>>(p, n); break;
     case Q4What::kRead:
-      q4_read_kernel<T, D><<<rows, kThreads, 0, st>>>(p, n, static_cast<T*>(k), static_cast<T*>(v));
+      q4_read_kernel<T, D><<<rows, kMoveThreads, 0, st>>>(p, n, static_cast<T*>(k), static_cast<T*>(v));
       break;
   }
   return cudaGetLastError();

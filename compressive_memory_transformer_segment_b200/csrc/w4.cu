@@ -37,9 +37,6 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kBlock = 128;  // channels of a packed block
 constexpr int kTile = 16;    // rows of a tile
 constexpr int kSMs = 148;
-#ifndef WS
-#define WS kSMs
-#endif
 
 // Scales and zeros of a row's NG groups (of 128 / NG channels) in one block, as
 // they lie in memory.
@@ -433,10 +430,10 @@ template <typename T, int NT, int NG>
 cudaError_t launch_tokens(const W4Problem& p, cudaStream_t st) {
   const unsigned tiles = (p.N + kTile - 1) / kTile, passes = (p.M + NT * 8 - 1) / (NT * 8);
   // 64 rows a CTA where that gives every SM one: 16 tokens, 4096 -> 16384 take
-  // WIDE_ROWS us so and WIDE_SPLIT us with the blocks shared out.  With 8 tokens or
+  // 21 us so and 25 us with the blocks shared out, 64 tokens 42 and 79.  With 8 tokens or
   // fewer there is little to share, and the split is as fast or faster.
   if constexpr (NT > 1) {
-    if (tiles >= (unsigned)(kRowWarps * WS)) {
+    if (tiles >= (unsigned)(kRowWarps * kSMs)) {
       constexpr int copies = 4 * NT * 8 * kBlock * (int)sizeof(T), sums = kRowWarps * kTile * (NT * 8 + 1) * 4;
       constexpr int bytes = copies > sums ? copies : sums;
       if (bytes > 48 * 1024) {
