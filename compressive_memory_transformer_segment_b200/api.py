@@ -9,6 +9,7 @@ Names follow the C ABI in include/infini_attn.h.
 """
 
 import ctypes
+import functools
 import os
 from typing import NamedTuple, Optional
 
@@ -445,12 +446,31 @@ def _workspace(t, dev):
     return _arg(t, "workspace", torch.uint8, (n,), dev), n
 
 
+@functools.lru_cache(maxsize=256)
+def _strides(shape):
+    """Strides of a contiguous tensor of this shape."""
+    out, n = [], 1
+    for s in reversed(shape):
+        out.append(n)
+        n *= max(s, 1)
+    return tuple(reversed(out))
+
+
 def _empty(shape, dtype, dev, stream):
-    """New memory for an output that ``stream`` writes: of that stream's pool."""
+    """New memory for an output that ``stream`` writes: of that stream's pool.
+    (empty_strided takes 1.6 us of the host's time, empty 2.5.)"""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty_strided(shape, _strides(shape), dtype=dtype, device=dev)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _output(t, name, dtype, shape, dev, stream):
+    """(tensor, address) of an output: the caller's, checked, or new memory."""
+    if t is None:
+        t = _empty(shape, dtype, dev, stream)
+        return t, t.data_ptr()
+    return t, _arg(t, name, dtype, shape, dev)
 
 
 def _like(t, stream):
@@ -499,18 +519,18 @@ def block_norm(r, w_next, eps, o=None, gate=None, scale=None, w_post=None, r_out
     vec, stat = (width,), shape[:-1]
     if not r.is_contiguous():
         raise ValueError("r must be contiguous")
-    if o is not None and r_out is None:
-        r_out = _like(r, stream)
-    if w_next is not None and h is None:
-        h = _like(r, stream)
+    r_out_ptr = h_ptr = None
+    if o is not None or r_out is not None:
+        r_out, r_out_ptr = _output(r_out, "r_out", dt, shape, dev, stream)
+    if w_next is not None or h is not None:
+        h, h_ptr = _output(h, "h", dt, shape, dev, stream)
     rp = _empty(stat, f32, dev, stream) if keep_rstd and w_post is not None else None
     rn = _empty(stat, f32, dev, stream) if keep_rstd and w_next is not None else None
     _call(load_library().infini_attn_block_norm, dev, stream,
           _arg(r, "r", dt, shape, dev), _arg(o, "o", dt, shape, dev), _arg(gate, "gate", dt, shape, dev),
           _arg(scale, "scale", f32, vec, dev), _arg(w_post, "w_post", f32, vec, dev),
           _arg(w_next, "w_next", f32, vec, dev), eps, r.numel() // max(width, 1), width, DTYPES[dt],
-          _arg(r_out, "r_out", dt, shape, dev), _arg(h, "h", dt, shape, dev),
-          rp.data_ptr() if rp is not None else None, rn.data_ptr() if rn is not None else None)
+          r_out_ptr, h_ptr, rp.data_ptr() if rp is not None else None, rn.data_ptr() if rn is not None else None)
     return r_out, h, rp, rn
 
 
@@ -639,10 +659,9 @@ class LinearW4:
         if dt not in DTYPES or not shape or shape[-1] != self.K:
             raise ValueError(f"x must be [..., {self.K}], bfloat16 or float32")
         ys = (*shape[:-1], self.N)
-        y = _empty(ys, dt, self.device, stream) if out is None else out
+        y, y_ptr = _output(out, "out", dt, ys, self.device, stream)
         _call(self._lib.infini_attn_linear_w4, self.device, stream, _arg(x, "x", dt, shape, self.device),
-              *self._weights, x.numel() // self.K, self.N, self.K, self.group, DTYPES[dt],
-              y.data_ptr() if out is None else _arg(out, "out", dt, ys, self.device))
+              *self._weights, x.numel() // self.K, self.N, self.K, self.group, DTYPES[dt], y_ptr)
         return y
 
     def qkv(self, x, H_q, H_kv, d, rope_cos=None, rope_sin=None, positions=None, q=None, k=None, v=None,
@@ -657,9 +676,9 @@ class LinearW4:
             raise ValueError("give both rotary tables or neither")
         B, L, _ = x.shape
         qs, ks = (B, H_q, L, d), (B, H_kv, L, d)
-        q = _empty(qs, dt, dev, stream) if q is None else q
-        k = _empty(ks, dt, dev, stream) if k is None else k
-        v = _empty(ks, dt, dev, stream) if v is None else v
+        q, q_ptr = _output(q, "q", dt, qs, dev, stream)
+        k, k_ptr = _output(k, "k", dt, ks, dev, stream)
+        v, v_ptr = _output(v, "v", dt, ks, dev, stream)
         n_pos = rope_cos.shape[0] if rope_cos is not None else 0
         rot = (n_pos, d // 2)
         dims = Dims(B, H_q, H_kv, L, d, d, DTYPES[dt])
@@ -667,7 +686,7 @@ class LinearW4:
               *self._weights, _arg(rope_cos, "rope_cos", torch.float32, rot, dev),
               _arg(rope_sin, "rope_sin", torch.float32, rot, dev), n_pos,
               _arg(positions, "positions", torch.int32, (B, L), dev), ctypes.byref(dims), self.K, self.group,
-              _arg(q, "q", dt, qs, dev), _arg(k, "k", dt, ks, dev), _arg(v, "v", dt, ks, dev))
+              q_ptr, k_ptr, v_ptr)
         return q, k, v
 
 
@@ -807,10 +826,9 @@ class CacheQ4:
         (k, v) [B, H_kv, n, d]."""
         dev, shape = self.device, (self.B, self.H_kv, int(n), self.d)
         dims = self._dims_ref(self.H_kv, int(n), dtype)
-        k = _empty(shape, dtype, dev, stream) if k is None else k
-        v = _empty(shape, dtype, dev, stream) if v is None else v
-        _call(self._lib.infini_attn_cache_q4_read, dev, stream, self._ref, dims, self.seg_len,
-              _arg(k, "k", dtype, shape, dev), _arg(v, "v", dtype, shape, dev))
+        k, k_ptr = _output(k, "k", dtype, shape, dev, stream)
+        v, v_ptr = _output(v, "v", dtype, shape, dev, stream)
+        _call(self._lib.infini_attn_cache_q4_read, dev, stream, self._ref, dims, self.seg_len, k_ptr, v_ptr)
         return k, v
 
     def state_update(self, n, M_in, z_in, rule, dtype=torch.bfloat16, M_out=None, z_out=None,
@@ -820,12 +838,12 @@ class CacheQ4:
         dev, f32 = self.device, torch.float32
         ms, zs = (self.B, self.H_kv, self.d, self.d), (self.B, self.H_kv, self.d)
         dims = self._dims_ref(self.H_kv, int(n), dtype)
-        M_out = _empty(ms, f32, dev, stream) if M_out is None else M_out
-        z_out = _empty(zs, f32, dev, stream) if z_out is None else z_out
+        M_out, M_ptr = _output(M_out, "M_out", f32, ms, dev, stream)
+        z_out, z_ptr = _output(z_out, "z_out", f32, zs, dev, stream)
         ws, ws_n = _workspace(workspace, dev)
         _call(self._lib.infini_attn_state_update_q4, dev, stream, self._ref, _arg(M_in, "M_in", f32, ms, dev),
               _arg(z_in, "z_in", f32, zs, dev), _rule(rule), dims, self.seg_len,
-              _arg(M_out, "M_out", f32, ms, dev), _arg(z_out, "z_out", f32, zs, dev), ws, ws_n)
+              M_ptr, z_ptr, ws, ws_n)
         return M_out, z_out
 
 

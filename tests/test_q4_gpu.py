@@ -11,7 +11,8 @@ V: the largest |value|):
             that of V;
   bf16      each probability times scale rounded to bf16, half a step 2^-8 of a
             term: together at most 2^-8 of R;
-  fp32      three parts hold 24 bits; the sums over n rows in fp32: 2^-23 V for
+  fp32      the parts that hold a probability keep it to 2^-22 of the largest (R
+            is at most twice V: 2^-21 V); the sums over n rows in fp32: 2^-23 V for
             each of the n / 16 / warps + 64 additions in a row, bounded by
             (n / 128 + 64) 2^-23 V;
   retrieval d additions of 2^-24 of the sums of magnitudes;
@@ -207,6 +208,30 @@ def test_append_and_read(cuda_lib, d, dtype):
     rk, _ = cache.read(S)
     assert torch.isnan(rk[2, 1, 16, :32]).all()
     assert torch.isnan(rk).sum() == 32
+
+
+def test_codes_at_ties_and_extreme_scales(cuda_lib):
+    """Codes, scales and minima stay the definition's where a quotient is a half
+    or next to one in fp32, and for scales from bf16's smallest to its largest."""
+    api, g = cuda_lib, np.random.default_rng(3)
+    n, d = 600, 64
+    x = np.zeros((1, 2, n, d // 32, 32), np.float32)  # heads as two more sets of groups
+    shape = x.shape[:-1]
+    power = g.integers(-133, 122, shape)
+    mant = g.integers(128, 256, shape)
+    s = oracle.bf16(np.ldexp(mant.astype(np.float64), power - 7).astype(np.float32)).astype(np.float32)
+    half = g.integers(0, 15, shape + (30,)).astype(np.float32) + np.float32(0.5)
+    at = (half * s[..., None]).astype(np.float32)
+    side = g.integers(0, 3, at.shape)
+    at = np.where(side == 0, np.nextafter(at, np.float32(0)), np.where(side == 1, at, np.nextafter(at, np.float32(np.inf))))
+    x[..., 0], x[..., 1], x[..., 2:] = 0.0, 15 * s, at
+    x = x.reshape(1, 2, n, d)
+    cache = api.CacheQ4.empty(1, 2, n, d)
+    k, v = torch.from_numpy(x), torch.from_numpy(x[:, ::-1].copy())
+    cache.append(k.cuda(), v.cuda(), torch.zeros(1, dtype=torch.int32, device="cuda"))
+    api.sync_status()
+    for got, want in zip(cache.tensors, packed((k, v))):
+        assert torch.equal(bits(got.cpu()), bits(want))
 
 
 @pytest.mark.parametrize("rule", ["linear", "delta"])
