@@ -325,14 +325,18 @@ w4_split_kernel(W4Problem p) {
 }
 
 // A CTA per 64 rows, one tile a warp, all blocks in turn: the tokens' channels of
-// a block are copied to shared memory once for the four tiles, two blocks ahead,
-// and a warp's codes are loaded three blocks ahead into registers.
+// a block are copied to shared memory once for the four tiles, two blocks ahead
+// (one ahead for 64 fp32 tokens, whose blocks are 32 KB: with three slots two CTAs
+// fit an SM, with four one, and 4096 -> 16384 takes 162 us against 311), and a
+// warp's codes are loaded three blocks ahead into registers.
 constexpr int kRowWarps = 4;
+template <typename T, int NT>
+constexpr int kRowStages = NT * 8 * kBlock * sizeof(T) >= 32768 ? 3 : 4;
 
 template <typename T, int NT, int NG>
 __global__ void __launch_bounds__(kRowWarps * 32, NT <= 2 ? 4 : NT == 4 ? 3 : 2)
 w4_rows_kernel(W4Problem p) {
-  constexpr int kTok = NT * 8, kStages = 4;
+  constexpr int kTok = NT * 8, kStages = kRowStages<T, NT>;
   constexpr int kRowBytes = kBlock * (int)sizeof(T), kPieces = kRowBytes / 16;  // of a token and block
   extern __shared__ __align__(16) uint8_t smem[];                               // [kStages][kTok][kRowBytes]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -434,7 +438,7 @@ cudaError_t launch_tokens(const W4Problem& p, cudaStream_t st) {
   // fewer there is little to share, and the split is as fast or faster.
   if constexpr (NT > 1) {
     if (tiles >= (unsigned)(kRowWarps * kSMs)) {
-      constexpr int copies = 4 * NT * 8 * kBlock * (int)sizeof(T), sums = kRowWarps * kTile * (NT * 8 + 1) * 4;
+      constexpr int copies = kRowStages<T, NT> * NT * 8 * kBlock * (int)sizeof(T), sums = kRowWarps * kTile * (NT * 8 + 1) * 4;
       constexpr int bytes = copies > sums ? copies : sums;
       if (bytes > 48 * 1024) {
         cudaError_t e =

@@ -64,7 +64,12 @@ CASES = [(1, 16, 128, 128, False, False), (1, 100, 4096, 128, True, True), (2, 1
          (7, 33, 120, 32, False, True), (8, 64, 136, 64, True, False), (9, 777, 1000, 32, True, True),
          (16, 48, 2048, 64, False, False), (17, 31, 1032, 128, True, True), (33, 1, 640, 64, True, False),
          (64, 130, 256, 32, True, True), (65, 16, 384, 128, False, False), (130, 19, 72, 64, True, True),
-         (5, 1030, 8192, 128, False, True)]
+         (5, 1030, 8192, 128, False, True),
+         # enough rows for 64 of them a CTA: every count of token tiles, blocks fewer
+         # than are loaded ahead and more, a last CTA with 1 to 3 tiles past the end
+         (9, 9473, 8, 32, True, True), (16, 9500, 1032, 64, False, True), (17, 9481, 136, 128, True, False),
+         (32, 9600, 640, 32, True, True), (33, 9489, 392, 64, True, True), (64, 9537, 520, 128, False, False),
+         (70, 9473, 256, 32, True, True)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -85,7 +90,8 @@ def test_linear(cuda_lib, M, N, K, group, zeros, bias, dtype):
 @pytest.mark.parametrize("B,L,H_q,H_kv,d,K,group,rope,positions",
                          [(1, 1, 2, 1, 128, 256, 128, True, True), (3, 1, 4, 2, 64, 200, 32, True, True),
                           (2, 5, 3, 1, 32, 128, 64, True, False), (2, 33, 2, 2, 64, 136, 64, False, False),
-                          (1, 9, 6, 2, 128, 1024, 128, True, True)])
+                          (1, 9, 6, 2, 128, 1024, 128, True, True),
+                          (3, 7, 60, 8, 128, 200, 32, True, True)])  # 64 rows a CTA
 def test_qkv(cuda_lib, B, L, H_q, H_kv, d, K, group, rope, positions, dtype):
     N = (H_q + 2 * H_kv) * d
     layer, w, b = layer_of(cuda_lib, N, K, group, True, True, seed=d)
