@@ -123,9 +123,10 @@ __device__ __forceinline__ void store_group(const float (&x)[8], int w, bool key
   __nv_bfloat162 par;
   par.y = __float2bfloat16_rn(lo);
   const float m = __bfloat162float(par.y);
-  par.x = __float2bfloat16_rn(__fmul_rn(fmaxf(__fsub_rn(hi, m), 0.f), 1.f / 15.f));
+  const float range = __fsub_rn(hi, m);
+  par.x = __float2bfloat16_rn(__fmul_rn(fmaxf(range, 0.f), 1.f / 15.f));
   const float s = __bfloat162float(par.x);
-  if (hi != hi) par = __floats2bfloat162_rn(NAN, NAN);
+  if (range != range) par = __floats2bfloat162_rn(NAN, NAN);
   // Codes: the quotient (x - m) / s rounded to the nearest integer, ties to even,
   // in 0..15.  An approximate quotient finds the half h = k + 1/2 nearest to it; the
   // sign of x - m - h s, which one fused operation gives exactly (h s fits 13 bits),
@@ -344,18 +345,22 @@ struct Ring {
       t.kcen[e] = __byte_perm(a, b, 0x5410);
     }
   }
-  // The largest scale of the values of 32 / (D / 8) .. rows of this lane, as bf16
-  // bits: the lanes' share of a slot's 16 rows together.
+  // The largest scale of this lane's share of a slot's 16 rows of values, as bf16
+  // bits; FINITE: of those that are neither infinite nor NaN.
+  template <bool FINITE>
   __device__ __forceinline__ uint32_t top_scale(int slot) const {
     const uint8_t* s = smem + slot * kSlot + 2 * kCodes + kParams;
     Raw<D / 16> half;  // half a row's parameters per lane
     uint32_t top = 0;
+    const auto add = [&](uint32_t w) {
+      if (!FINITE || (w & 0x7f80u) != 0x7f80u) top = __vmaxu2(top, w);
+    };
     if constexpr (D == 32) {
-      top = *reinterpret_cast<const uint32_t*>(s + (lane & 15) * 4);
+      add(*reinterpret_cast<const uint32_t*>(s + (lane & 15) * 4));
     } else {
       half.load(s + lane * (D / 16));
 #pragma unroll
-      for (int j = 0; j < D / 64; ++j) top = __vmaxu2(top, half.word(j));
+      for (int j = 0; j < D / 64; ++j) add(half.word(j));
     }
     return top & 0xffffu;  // the scales are the low halves
   }
@@ -561,7 +566,7 @@ struct Attention {
   __device__ __forceinline__ void raise(uint32_t top) {
     top = __reduce_max_sync(0xffffffffu, top);
     if (top <= limit) return;
-    const int to = max(min((int)(top >> 7), 255) - 127, -120);
+    const int to = max(min((int)(top >> 7) - 127, 126), -120);
     const float down = exp2f((float)(pe - to));
 #pragma unroll
     for (int j = 0; j < 2 * NJ; ++j)
@@ -636,14 +641,16 @@ struct Attention {
   }
 
   // Probabilities (powers of two relative to a reference m, at most 2^kLead) of
-  // a tile from its scores x; top: the largest scale of this lane's rows, as
-  // bf16 bits.  A maximum is taken over the warp only when a score leaves that
+  // a tile from its scores x; the tile lies in `slot`.  A maximum is taken over the warp only when a score leaves that
   // room (and by the first rows), not for every tile.
-  __device__ __forceinline__ void probabilities(const float (&x)[4], uint32_t top, float (&pr)[4]) {
+  __device__ __forceinline__ void probabilities(const float (&x)[4], const Ring<D>& ring, int slot,
+                                                float (&pr)[4]) {
     const float top0 = fmaxf(x[0], x[2]), top1 = fmaxf(x[1], x[3]);
-    if (__builtin_expect(__any_sync(0xffffffffu, fmaxf(top0 - m[0], top1 - m[1]) > kLead || top > limit), 0)) {
+    if (__builtin_expect(__any_sync(0xffffffffu, fmaxf(top0 - m[0], top1 - m[1]) > kLead ||
+                                                    ring.template top_scale<false>(slot) > limit), 0)) {
       rebase(top0, top1);
-      raise(top);
+      // (A group whose scale is NaN or infinite has no say in the others' unit.)
+      raise(ring.template top_scale<true>(slot));
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) pr[e] = exp2_approx(x[e] - m[e & 1]);
@@ -676,7 +683,7 @@ struct Attention {
         __syncwarp();  // every lane has read the slot
       }
       ring.next(before, x + R::kStages - 1);
-      probabilities(s, ring.top_scale(slot), pr);
+      probabilities(s, ring, slot, pr);
       before = slot;
       slot = slot + 1 < R::kStages ? slot + 1 : 0;
     }
@@ -716,7 +723,7 @@ struct Share {
     // Near enough that a turn or two set it right.
     uint32_t k = min((uint32_t)((float)u * ((float)ctas / (float)units)), ctas - 1);
     while (first(k) > u) --k;
-    while (first(k + 1) <= u) ++k;
+    while (k + 1 < ctas && first(k + 1) <= u) ++k;
     return k;
   }
 };
@@ -735,7 +742,7 @@ __device__ __forceinline__ void locate(const Q4Problem& p, uint32_t segs, Share&
   const uint32_t want = share.first(blockIdx.x);
   start = 0;
 #pragma unroll 1
-  for (int b0 = 0;; b0 += 32) {
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
     if (p.B > 32) mine = b0 + lane < p.B ? stream_units(p, b0 + lane) * segs : 0;
     uint32_t incl = mine;
 #pragma unroll
@@ -751,6 +758,7 @@ __device__ __forceinline__ void locate(const Q4Problem& p, uint32_t segs, Share&
     }
     start += __shfl_sync(0xffffffffu, incl, 31);
   }
+  share.ctas = 0;  // (only if the positions changed meanwhile)
 }
 
 // A run of units of one segment, and the segment's place.
@@ -964,10 +972,14 @@ q4_decode_kernel(Q4Problem p) {
     int k0 = 0, k1 = 0;
     if (more) {
       uint32_t n = stream_units(p, run.b);
-      while (run.u >= run.off + segs * n) {
+      while (run.u >= run.off + segs * n && (int)run.b + 1 < p.B) {
         run.off += segs * n;
         n = stream_units(p, ++run.b);
       }
+      run.pos = p.pos[run.b];
+      // Positions that change while the step runs give no result worth having, but
+      // must not lead out of the buffer either.
+      if (run.pos < 0 || run.pos >= p.S || n <= (uint32_t)p.lead || run.u >= run.off + segs * n) return;
       run.seg = (run.u - run.off) / n;
       n -= p.lead;
       run.s0 = run.off + run.seg * (n + p.lead) + p.lead;
@@ -976,7 +988,6 @@ q4_decode_kernel(Q4Problem p) {
       run.u = max(run.u, run.s0);
       more = run.u < run.end;  // (else only of a segment's lead: its rows are the next CTA's)
       if (more) {
-        run.pos = p.pos[run.b];
         run.hk = zc == 1 ? run.seg : run.seg / zc;
         run.hq0 = run.hk * g + (run.seg - run.hk * zc) * kHeads;
         run.ng = min(kHeads, (run.hk + 1) * g - run.hq0);

@@ -491,8 +491,10 @@ INFINI_API int infini_attn_decode_step(const void* q_t, const void* k_t, const v
  *   scale q + minimum,  q in 0..15,
  * with minimum = bf16(the group's least value), scale =
  * bf16((greatest - minimum) / 15) and q = (value - minimum) / scale to the
- * nearest, ties to even, cut to 0..15 (0 where scale is 0); fp32 arithmetic.  A group with a NaN,
- * an infinity or a range beyond fp32 reads back as NaN.
+ * nearest, ties to even, cut to 0..15 (0 where scale is 0); fp32 arithmetic.
+ * A group with a NaN, an infinity or a range beyond fp32 reads back as NaN, and
+ * as nothing else: attended values of other groups keep their results.  Scales
+ * that a caller writes must not be negative.
  *   k_codes, v_codes   device [B, H_kv, seg_len, d / 2] bytes
  *   k_scale, v_scale   device bf16 [B, H_kv, seg_len, d / 32, 2]: scale,
  *                      minimum
@@ -564,7 +566,7 @@ INFINI_API size_t infini_attn_decode_q4_workspace_bytes(const infini_dims_t* dim
  *                segment is full (pos[b] = seg_len - 1) the caller updates
  *                them with infini_attn_state_update_q4.
  *   pos          device int32 [B], read by the kernel: a captured step serves
- *                every position
+ *                every position.  It must not change while the step runs.
  *   dims         B, H_q (a multiple of H_kv), H_kv, d_k = d_v = d, dtype;
  *                dims->L is ignored
  *   workspace    infini_attn_decode_q4_workspace_bytes bytes, 256-byte aligned
@@ -572,7 +574,9 @@ INFINI_API size_t infini_attn_decode_q4_workspace_bytes(const infini_dims_t* dim
  *                (stream-ordered allocation, zeroed by the call)
  *   stream       cudaStream_t; asynchronous.
  * The buffer's arrays, out_t and the workspace overlap nothing.  Sums run in a
- * fixed order: repeated calls are bitwise equal.  Errors: those of
+ * fixed order: repeated calls are bitwise equal.  The order follows from all the
+ * positions (streams share the GPU by their lengths), so a stream's last bits
+ * may differ with its neighbours' positions.  Errors: those of
  * infini_attn_decode_step. */
 INFINI_API int infini_attn_decode_step_q4(const void* q_t, const void* k_t, const void* v_t,
                                           const float* beta, const infini_cache_q4_t* cache,

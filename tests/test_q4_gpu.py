@@ -178,6 +178,86 @@ def test_position_out_of_range_is_reported_and_left_alone(cuda_lib):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_lost_group_takes_nothing_else_with_it(cuda_lib, dtype):
+    """A group of values with a NaN or an infinity in an attended row: its 32
+    channels are NaN, the others what they are without it, whatever the scales'
+    size (first and last rows, so that some are seen before and some after)."""
+    api = cuda_lib
+    H, d, S = 2, 128, 400
+    for size in (1.0, 2.0 ** 60, 2.0 ** 118):
+        keys, vals = randn(1, H, S, d, seed=1), randn(1, H, S, d, seed=2) * size
+        vals[0, 0, 3, 40], vals[0, 0, 390, 50], vals[0, 1, 200, 96:] = math.nan, -math.inf, math.inf
+        cache = api.CacheQ4(*(t.cuda() for t in packed((keys, vals))))
+        rows = [randn(1, n, d, seed=3 + n, dtype=dtype) for n in (H, H)]
+        q = randn(1, 2 * H, d, seed=9, dtype=dtype)
+        M, z = torch.zeros(1, H, d, d), torch.ones(1, H, d)
+        beta, pos = torch.full((2 * H,), -100.0), torch.tensor([S - 1], dtype=torch.int32)
+        out = f64(api.decode_step_q4(q.cuda(), rows[0].cuda(), rows[1].cuda(), beta.cuda(), cache, pos.cuda(),
+                                     M.cuda(), z.cuda()))
+        api.sync_status()
+        K, V = values_of(cache)
+        lost = np.isnan(V).any(2)  # [1, H, d]
+        assert lost.sum() == 64
+        ref = oracle.decode_step_q4(f64(q), K, np.nan_to_num(V, nan=0.0), [S - 1], f64(beta), f64(M), f64(z))
+        for h in range(2 * H):
+            gone = lost[0, h // 2]
+            assert np.isnan(out[0, h, gone]).all()
+            top = np.max(np.abs(V[0, h // 2][:, ~gone]))
+            # The docstring's bounds with R <= 2 V, A <= 32, n = 400: bf16 (2^-7 + 2^-13
+            # + 2^-8) V < 2^-6 V, fp32 (2^-13 + 2^-16 + 2^-24) V < 2^-12 V.
+            err = np.abs(out[0, h] - ref[0, h])[~gone]
+            assert np.all(err <= (2.0 ** -6 if dtype == "bf16" else 2.0 ** -12) * top)
+
+
+def test_offsets_beyond_32_bits(cuda_lib):
+    """Rows whose offset passes 2^32 bytes and 2^31 elements: of the last of many
+    streams, and of one long stream all of whose rows count."""
+    api, d = cuda_lib, 128
+    # 40 x 8 x 2^18 rows of 64 bytes; the last stream alone is attended
+    B, H, S = 40, 8, 1 << 18
+    cache = api.CacheQ4.empty(B, H, S, d)
+    n = 70
+    k, v = randn(1, H, n, d, seed=1), randn(1, H, n, d, seed=2)
+    at = torch.full((B,), -1, dtype=torch.int32)
+    at[-1] = S - n
+    ks, vs = torch.zeros(B, H, n, d), torch.zeros(B, H, n, d)
+    ks[-1], vs[-1] = k[0], v[0]
+    cache.append(ks.cuda(), vs.cuda(), at.cuda())
+    api.sync_status()
+    for got, want in zip(cache.tensors, packed((k, v))):
+        assert torch.equal(bits(got[-1, :, S - n:].cpu()), bits(want[0]))
+        assert not got[-1, :, S - n - 100:S - n].any() and not got[:4].any()
+    del cache
+    # one stream of 2^26 + 77 rows, zeros but for the first and the last 64
+    S = (1 << 26) + 77
+    cache = api.CacheQ4.empty(1, 1, S, d)
+    ends = packed((randn(1, 1, 128, d, seed=4), randn(1, 1, 128, d, seed=5)))
+    for t, e in zip(cache.tensors, ends):
+        t[0, 0, :64], t[0, 0, S - 65:S - 1] = e[0, 0, :64].cuda(), e[0, 0, 64:].cuda()
+    q = randn(1, 2, d, seed=6)
+    kt, vt = randn(1, 1, d, seed=7), randn(1, 1, d, seed=8)
+    q *= 7.0  # largest scores of 17 and 18: they and the zeros count alike
+    pos, beta = torch.tensor([S - 1], dtype=torch.int32), torch.full((2,), -100.0)
+    out = f64(api.decode_step_q4(q.cuda(), kt.cuda(), vt.cuda(), beta.cuda(), cache, pos.cuda(),
+                                 torch.zeros(1, 1, d, d, device="cuda"), torch.ones(1, 1, d, device="cuda")))
+    api.sync_status()
+    tail = [torch.cat((t[0, 0, :64], t[0, 0, S - 65:])).cpu() for t in cache.tensors]
+    K, V = (oracle.cache_values(oracle.codes_of(c.numpy(), d, bit, d).astype(np.float64), f64(s)[..., 0],
+                                f64(s)[..., 1])
+            for c, s, bit in ((tail[0], tail[1], oracle.key_bit), (tail[2], tail[3], oracle.value_bit)))
+    for h in range(2):
+        s = K @ f64(q)[0, h] / math.sqrt(d)
+        m = max(s.max(), 0.0)
+        p = np.exp(s - m)
+        ref = p @ V / (p.sum() + (S - len(s)) * math.exp(-m))
+        A = (np.abs(K) @ np.abs(f64(q)[0, h])).max() / math.sqrt(d) * math.log2(math.e)
+        # the zeros' sum: a lane adds 2 of every 16 rows that its warp has, of 296 CTAs' 4 or
+        # more: below 2^12 additions in a row
+        slack = (2 * 2.0 ** -19 * A + 2.0 ** 12 * 2.0 ** -23) * np.abs(V).max()
+        assert 15.0 < m < 20.0 and np.all(np.abs(out[0, h] - ref) <= slack), float(np.abs(out[0, h] - ref).max())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("d", [32, 64, 128])
 def test_append_and_read(cuda_lib, d, dtype):
     api = cuda_lib
