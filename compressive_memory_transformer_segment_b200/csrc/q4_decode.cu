@@ -7,23 +7,29 @@
 //   score_r = sum_j s_rj (sum over j of q_r x) + m_rj (sum over j of x),
 //   a_dot   = sum_r p_r v_r / sum_r p_r,
 //   sum_r p_r v_r[e] = sum_r (p_r s_rj) q_r[e] + sum_r p_r m_rj   (e in group j)
-// so both products run over the codes themselves (integers, exact in bf16) on
-// the tensor cores, with the scales on the outside of the first and folded
-// into the probabilities of the second.  Probabilities times scale are
-// rounded to bf16 for bf16 heads (2^-8 of each term, as in the bf16 forward);
-// fp32 heads carry queries and probabilities as three bf16 parts each.
+// so both products run over the codes themselves on the tensor cores, with the
+// scales on the outside of the first and folded into the probabilities of the
+// second.  Queries and probabilities times scale meet the codes as fp16, in its
+// range by powers of two: one part for bf16 heads (2^-12 of a term, less than
+// their own rounding), two for fp32 heads (2^-23).
 //
-// Bound by the buffer's bytes (5 bits per value): with 4 query heads per KV
-// head a CUDA-core version would need 8 multiply-adds per value besides the
-// conversions, about 1.5 times what the memory allows; as matrix products
-// (16 rows x 8 heads, mma.sync) the arithmetic is left to the conversions.
-// One warp takes 16 rows at a time:
+// The floor is the buffer's bytes (5 bits per value), but what bounds it at 64
+// streams is the instructions around them: with 4 query heads per KV head half of
+// each product's 8 columns are empty, and making operands of the codes, the
+// scales and the probabilities take more cycles than the bytes.  A CUDA-core
+// version would need 8 multiply-adds per value besides the conversions.
+// One warp takes 16 rows at a time (mma.sync: 16 rows x 8 heads):
 //   S^T = K Q^T   rows of codes are the A operand (lane 4 i + c: rows i, i + 8),
 //   O^T = V^T P^T V's codes are the A operand with the rows along k, P^T the
 //                 B operand: the scores' fragments, transposed in registers.
-// The buffer's layout is such that a lane's fragments are one contiguous load
-// per row (see the header), so rows go from global memory to the tensor cores
-// without shared memory; the next 16 rows are loaded while these are used.
+// The layout (see the header) is such that a lane's fragments are contiguous.
+// Rows come by asynchronous copies through a ring in shared memory, a warp's own
+// (no barrier), three tiles ahead.
+//
+// Measured (device time): 2 streams at the end of 2048-row segments, 32/8 heads of
+// 128, 13 us (6 MB: latency alone); 64 streams at ragged positions below 8192 105
+// us for 370 MB, 3.5 TB/s, 0.54 of the copy rate; 8 x 8 x 1500 rows appended and read
+// back 35 us for 137 MB, 3.9 TB/s (bound by the instructions that choose the codes).
 //
 // Grid: the rows of all (stream, KV head, chunk of 8 query heads) are shared out
 // in equal parts over as many CTAs as the GPU holds, whatever the streams'

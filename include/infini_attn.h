@@ -342,10 +342,10 @@ INFINI_API int infini_attn_linear_w4(const void* x, const void* packed, const vo
  *              as for infini_attn_qkv_project, but the tables have n_pos rows
  *   n_pos      rows of the tables; >= L if positions is NULL
  *   positions  device int32 [B, L], the table row of each token, or NULL
- *              (token t of every batch row uses row t); needs the tables.  A
- *              value outside [0, n_pos) is reported by
- *              infini_attn_sync_status (INFINI_ERR_RANGE) and the token's
- *              heads are not rotated.
+ *              (token t of every batch row uses row t); needs the tables.  -1
+ *              (an idle stream): the token's heads are not rotated; any other
+ *              value outside [0, n_pos): the same, and reported by
+ *              infini_attn_sync_status (INFINI_ERR_RANGE).
  *   dims       B, H_q, H_kv, L, d_k = d_v = d in {32, 64, 128}, dtype
  *   q, k, v    device [B, H_q, L, d], [B, H_kv, L, d], [B, H_kv, L, d],
  *              element type dims->dtype

@@ -132,6 +132,9 @@ def test_position_out_of_range_is_reported(cuda_lib):
         cuda_lib.sync_status()
     assert e.value.status == cuda_lib.ERR_RANGE
     cuda_lib.sync_status()  # reported once
+    idle = layer.qkv(x, 2, 1, 32, cos, sin, pos.clamp_max(3) * 0 - 1)  # no report
+    cuda_lib.sync_status()
+    assert all(torch.equal(a, b) for a, b in zip(idle, layer.qkv(x, 2, 1, 32)))
     plain = layer.qkv(x, 2, 1, 32)
     assert torch.equal(q[1:], plain[0][1:]) and torch.equal(k[1:], plain[1][1:])
     assert not torch.equal(q[0], plain[0][0])
