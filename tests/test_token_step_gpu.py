@@ -6,9 +6,10 @@ Each stage is compared with the float64 oracle on that stage's own inputs (the
 GPU's output of the stage before), in fp32, so that a rounding of one stage is
 not counted in the next.  Tolerances: a norm or projection of K terms 2^-23 K
 of the sum of magnitudes (K = 96 and 128 here: below 2^-16 of it, taken
-against the output's scale of a few units: 1e-4); the decode step 1e-4 (scores'
-magnitudes below 2^7 times 2^-19, values below 4: below 2^-9... per
-probability, of which the mean of n <= 11 near-equal values keeps less)."""
+against the output's scale of a few units: 1e-4); the decode step 1e-4: scores'
+magnitudes stay below 2^4, so 2^-19 of them on either side of a probability and
+values below 4 make 2 x 2^-15 x 4 = 2^-12 at the very most, and the mean over a
+few rows whose signs differ keeps less than a quarter of it."""
 
 import numpy as np
 import pytest
