@@ -21,13 +21,16 @@
 // makes the rows unaligned), and walks over the rows with its columns' weights in
 // registers.  Its next rows are on their way meanwhile: every thread copies its
 // own pieces to shared memory asynchronously (so no barrier goes with them) and
-// reads them back when their turn comes.  All statistics and sums in fp32.
+// reads them back when their turn comes.  All statistics and sums in fp32, by the
+// packed operations on two neighbouring channels (backward, 16384 x 4096: 209 us,
+// 234 with single ones, whose instructions filled 60% of the cycles).
 //
 // Measured (device time, bf16, every part): forward 65536 x 4096 462 us, 5.8 TB/s;
 // backward 16384 x 4096 209 us, 5.1 TB/s, 8192 x 768 28 us, 3.6 TB/s; one token 3.3
 // us.  What keeps the backward below the copy rate: its sums and weights take the
 // registers of all but 16 warps per SM, which two reductions a row stop in turn.
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "kernels.h"
 #include "pdl.cuh"
 
@@ -39,46 +42,6 @@ constexpr int kSMs = 148;
 constexpr int kMaxThreads = 512;
 constexpr int kFwdThreads = 1024;  // threads per SM that the registers allow
 constexpr int kBwdThreads = 512;   // (8192 x 768: 28 us; with 640, by fewer registers, 31)
-
-// Two neighbouring channels at a time: one instruction of the packed fp32 forms
-// does both (single ones for pieces of one element).  Backward, 16384 x 4096: 209
-// us so, 234 with single operations, whose instructions filled 60% of the cycles.
-template <int V> struct LaneOf { using type = float2; };
-template <> struct LaneOf<1> { using type = float; };
-__device__ __forceinline__ unsigned long long bits(float2 x) {
-  return (unsigned long long)__float_as_uint(x.y) << 32 | __float_as_uint(x.x);
-}
-__device__ __forceinline__ float2 pair(unsigned long long x) {
-  return {__uint_as_float((unsigned)x), __uint_as_float((unsigned)(x >> 32))};
-}
-__device__ __forceinline__ float2 mul(float2 a, float2 b) {
-  unsigned long long d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)));
-  return pair(d);
-}
-__device__ __forceinline__ float2 add(float2 a, float2 b) {
-  unsigned long long d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)));
-  return pair(d);
-}
-__device__ __forceinline__ float2 fma(float2 a, float2 b, float2 c) {
-  unsigned long long d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
-  return pair(d);
-}
-__device__ __forceinline__ float mul(float a, float b) { return a * b; }
-__device__ __forceinline__ float add(float a, float b) { return a + b; }
-__device__ __forceinline__ float fma(float a, float b, float c) { return fmaf(a, b, c); }
-__device__ __forceinline__ float sum(float2 x) { return x.x + x.y; }
-__device__ __forceinline__ float sum(float x) { return x; }
-__device__ __forceinline__ void put(float* to, int e, float2 x) {
-  to[2 * e] = x.x;
-  to[2 * e + 1] = x.y;
-}
-__device__ __forceinline__ void put(float* to, int e, float x) { to[e] = x; }
-template <typename L> __device__ __forceinline__ L both(float x);
-template <> __device__ __forceinline__ float2 both<float2>(float x) { return {x, x}; }
-template <> __device__ __forceinline__ float both<float>(float x) { return x; }
 
 template <int BYTES> struct RawVec;
 template <> struct RawVec<2> { using type = unsigned short; };

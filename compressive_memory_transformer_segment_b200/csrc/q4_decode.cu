@@ -29,7 +29,7 @@
 // Measured (device time): 2 streams at the end of 2048-row segments, 32/8 heads of
 // 128, 13 us (6 MB: latency alone); 64 streams at ragged positions below 8192 105
 // us for 370 MB, 3.5 TB/s, 0.54 of the copy rate; 8 x 8 x 1500 rows appended and read
-// back 35 us for 137 MB, 3.9 TB/s (bound by the instructions that choose the codes).
+// back 34 us for 137 MB, 4.0 TB/s (bound by the instructions that choose the codes).
 //
 // Grid: the rows of all (stream, KV head, chunk of 8 query heads) are shared out
 // in equal parts over as many CTAs as the GPU holds, whatever the streams'
@@ -40,6 +40,7 @@
 #include <cuda_fp16.h>
 
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "kernels.h"
 #include "q4_common.cuh"
 
@@ -140,14 +141,15 @@ __device__ __forceinline__ void store_group(const float (&x)[8], int w, bool key
   // first changes nothing: where x - m is not h s it differs by 2^-24 of it or
   // more, and half a step at h is less.  Ties are not rare (bf16 values and a bf16
   // scale: about one group in eight has one), so no branch looks for them.
-  float d[8], s1 = s;
+  float2 d[4];
+  float s1 = s;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) d[e] = __fsub_rn(x[e], m);
+  for (int e = 0; e < 4; ++e) d[e] = add({x[2 * e], x[2 * e + 1]}, {-m, -m});
   if (!(s >= 0x1p-100f && s < INFINITY)) {  // all codes 0, or a scale whose reciprocal overflows
     const bool none = !(s > 0.f && s < INFINITY);
     s1 = none ? 1.f : s * 0x1p100f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) d[e] = none ? 0.f : d[e] * 0x1p100f;
+    for (int e = 0; e < 4; ++e) d[e] = none ? float2{0.f, 0.f} : mul(d[e], {0x1p100f, 0x1p100f});
   }
   float inv;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s1));
@@ -155,11 +157,16 @@ __device__ __forceinline__ void store_group(const float (&x)[8], int w, bool key
   constexpr float kRound = 12582912.f;  // 1.5 2^23: a sum with it has an integer in its low bits
   uint32_t q[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float u = fmaf(__saturatef(fmaf(d[e], inv, -0.5f / 14.f)), 14.f, kRound);
-    const float r = fmaf(-__fadd_rn(__fsub_rn(u, kRound), 0.5f), s1, d[e]);
-    q[e] = __float_as_uint(u) & 15u;
-    q[e] += __float_as_int(r) + (int)(q[e] & 1u) > 0;  // r > 0, or 0 and k odd
+  for (int e = 0; e < 4; ++e) {
+    const float2 part = {__saturatef(fmaf(d[e].x, inv, -0.5f / 14.f)), __saturatef(fmaf(d[e].y, inv, -0.5f / 14.f))};
+    const float2 u = fma(part, {14.f, 14.f}, {kRound, kRound});
+    // (k - 2^23 3 / 2 and the half in two steps: the constant of one is no fp32.)
+    const float2 r = fma(add(add(u, {-kRound, -kRound}), {0.5f, 0.5f}), {-s1, -s1}, d[e]);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t k = __float_as_uint(h ? u.y : u.x) & 15u;
+      q[2 * e + h] = k + (__float_as_int(h ? r.y : r.x) + (int)(k & 1u) > 0);  // r > 0, or 0 and k odd
+    }
   }
   if (!active) return;
   uint32_t word = 0;
@@ -1164,12 +1171,15 @@ __device__ __forceinline__ void read_rows(const uint8_t* codes, const __nv_bfloa
     const float s = __uint_as_float(par[e] << 16), m = __uint_as_float(par[e] & 0xffff0000u);
     float out[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {  // the codes from the lowest bits on: 2^23 + 16^(i % 4) code, less 2^23
+    for (int i = 0; i < 4; ++i) {  // codes i and i + 4 from the lowest bits on: 2^23 + 16^i code, less 2^23
       constexpr float kBase = 8388608.f;
-      const uint32_t bits = (i < 4 ? word[e] : word[e] >> 16) & (15u << 4 * (i & 3));
-      const float at = 1.f / (1 << 4 * (i & 3));
-      const float q = fmaf(__uint_as_float(bits | 0x4b000000u), at, -kBase * at);
-      out[KEY ? (i < 4 ? 2 * i : 2 * i - 7) : i] = fmaf(s, q, m);
+      const float at = 1.f / (1 << 4 * i);
+      const uint32_t mask = 15u << 4 * i;
+      const float2 n = {__uint_as_float((word[e] & mask) | 0x4b000000u),
+                        __uint_as_float((word[e] >> 16 & mask) | 0x4b000000u)};
+      const float2 y = fma({s, s}, fma(n, {at, at}, {-kBase * at, -kBase * at}), {m, m});
+      out[KEY ? 2 * i : i] = y.x;
+      out[KEY ? 2 * i + 1 : i + 4] = y.y;
     }
     if (e * kStep < left) store8(to + e * (kStep * D), out);
   }
