@@ -456,6 +456,14 @@ def _strides(shape):
     return tuple(reversed(out))
 
 
+@functools.lru_cache(maxsize=256)
+def _dims_ref(B, H_q, H_kv, L, d, dtype):
+    """Reference to the struct of these sizes (calls only read it)."""
+    if dtype not in DTYPES:
+        raise ValueError("dtype must be bfloat16 or float32")
+    return ctypes.byref(Dims(B, H_q, H_kv, L, d, d, DTYPES[dtype]))
+
+
 def _empty(shape, dtype, dev, stream):
     """New memory for an output that ``stream`` writes: of that stream's pool.
     (empty_strided takes 1.6 us of the host's time, empty 2.5.)"""
@@ -681,12 +689,11 @@ class LinearW4:
         v, v_ptr = _output(v, "v", dt, ks, dev, stream)
         n_pos = rope_cos.shape[0] if rope_cos is not None else 0
         rot = (n_pos, d // 2)
-        dims = Dims(B, H_q, H_kv, L, d, d, DTYPES[dt])
         _call(self._lib.infini_attn_qkv_project_w4, dev, stream, _arg(x, "x", dt, x.shape, dev),
               *self._weights, _arg(rope_cos, "rope_cos", torch.float32, rot, dev),
               _arg(rope_sin, "rope_sin", torch.float32, rot, dev), n_pos,
-              _arg(positions, "positions", torch.int32, (B, L), dev), ctypes.byref(dims), self.K, self.group,
-              q_ptr, k_ptr, v_ptr)
+              _arg(positions, "positions", torch.int32, (B, L), dev), _dims_ref(B, H_q, H_kv, L, d, dt), self.K,
+              self.group, q_ptr, k_ptr, v_ptr)
         return q, k, v
 
 
@@ -781,7 +788,6 @@ class CacheQ4:
                                   _arg(v_codes, "v_codes", torch.uint8, k_codes.shape, dev),
                                   _arg(v_scale, "v_scale", torch.bfloat16, scale, dev))
         self._ref = ctypes.byref(self._ptrs)
-        self._dims = {}  # per (H_q, L, dtype): the struct the calls take
         self._lib = load_library()
 
     @classmethod
@@ -800,16 +806,7 @@ class CacheQ4:
         return CacheQ4(*(t[b:b + 1] for t in self.tensors))
 
     def _dims_ref(self, H_q, L, dtype):
-        key = (H_q, L, dtype)
-        ref = self._dims.get(key)
-        if ref is None:
-            if dtype not in DTYPES:
-                raise ValueError("dtype must be bfloat16 or float32")
-            ref = ctypes.byref(Dims(self.B, H_q, self.H_kv, L, self.d, self.d, DTYPES[dtype]))
-            if len(self._dims) > 64:
-                self._dims.clear()
-            self._dims[key] = ref
-        return ref
+        return _dims_ref(self.B, H_q, self.H_kv, L, self.d, dtype)
 
     def append(self, k, v, pos, stream=None):
         """infini_attn_cache_q4_append: k, v [B, H_kv, n, d] (bfloat16 or
