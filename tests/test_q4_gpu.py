@@ -131,6 +131,11 @@ STEPS = [
     (2, 9, 9, 128, 64, [40, 63]),                     # one head per KV head
     (1, 4, 1, 128, 2048, [2047]),
     (1, 2, 1, 32, 5000, [4999]),
+    (4, 4, 2, 32, 16, [-1, -1, -1, -1]),              # nothing to do
+    (70, 2, 1, 32, 300, [(37 * b) % 301 - 1 for b in range(70)]),     # more streams than a warp has lanes
+    (33, 1, 1, 64, 2000, [-1] * 32 + [1999]),         # the last one alone
+    (1100, 1, 1, 32, 40, [b % 41 - 1 for b in range(1100)]),          # more segments than CTAs
+    (600, 3, 3, 32, 140, [139 - b % 7 for b in range(600)]),
 ]
 
 
