@@ -259,3 +259,34 @@ def test_binding_refuses(cuda_lib):
         forward(cuda_lib, dict(xd, o=None))
     with pytest.raises(cuda_lib.InfiniError):
         cuda_lib.block_norm(xd["r"], xd["w_next"], 0.0)
+
+
+def test_offsets_beyond_32_bits(cuda_lib):
+    """131075 rows of 16384: elements past 2^31.  The last rows' results, forward
+    and backward, are those of the rows alone (rows do not affect one another)."""
+    api, rows, width, n = cuda_lib, (1 << 17) + 3, 16384, 5
+    x, d = make(n, width, "bf16", dict(ALL, gate=False))
+    big = torch.zeros(rows, width, dtype=torch.bfloat16, device="cuda")
+
+    def placed(t):
+        out = torch.zeros_like(big)
+        out[-n:] = t.cuda()
+        return out
+
+    small = dev(x)
+    r_out, h, rp, rn = forward(api, small)
+    large = dict(small, r=placed(x["r"]), o=placed(x["o"]))
+    got = forward(api, large)
+    api.sync_status()
+    for a, b in zip(got, (r_out, h, rp, rn)):
+        assert torch.equal(a[-n:], b)
+    assert not got[0][:-n].any() and not got[1][:-n].any()
+    grads = backward(api, small, dev(d), r_out, rp, rn)
+    all_grads = backward(api, large, dict(dr_out=placed(d["dr_out"]), dh=placed(d["dh"])), got[0], got[2], got[3])
+    api.sync_status()
+    for a, b in ((all_grads.dr, grads.dr), (all_grads.do, grads.do)):
+        assert torch.equal(a[-n:], b) and not a[:-n].any()
+    # Sums of 5 rows among zeros, in another order: 8 roundings of 2^-24 of the largest terms.
+    for a, b in ((all_grads.dscale, grads.dscale), (all_grads.dw_post, grads.dw_post),
+                 (all_grads.dw_next, grads.dw_next)):
+        assert float((a - b).abs().max()) <= 8 * 2.0 ** -24 * 5 * float(b.abs().max())

@@ -178,6 +178,23 @@ def test_tokens_are_independent_and_repeats_equal(cuda_lib):
     assert torch.equal(y2[keep], y[keep]) and torch.isnan(y2[3]).all()
 
 
+@pytest.mark.parametrize("M", [1, 12])
+def test_weights_beyond_32_bits(cuda_lib, M):
+    """2^20 + 3 rows of 4096 codes: packed offsets pass 2^31 bytes."""
+    N, K = (1 << 20) + 3, 4096
+    g = torch.Generator(device="cuda").manual_seed(M)
+    packed = torch.randint(0, 256, (N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    scales = (0.01 + torch.rand(N, K // 128, generator=g, device="cuda")).bfloat16()
+    x = tokens(M, K, "bf16")
+    y = cuda_lib.LinearW4(packed, scales, None, K)(x.cuda())
+    cuda_lib.sync_status()
+    for rows in (slice(0, 5), slice(N - 40, N)):
+        w = oracle.w4_weight(packed[rows].cpu().numpy(), f64(scales[rows]), None, K, 128)
+        ref = f64(x) @ w.T
+        err = np.abs(f64(y[:, rows]) - ref) - HALF["bf16"] * np.abs(ref) - slack_of(f64(x), w, np.zeros(len(w)))
+        assert np.all(err <= 0), float(err.max())
+
+
 def test_other_stream_captured_graph_and_other_shapes(cuda_lib):
     layer, _, _ = layer_of(cuda_lib, 256, 1024, 128, True, True)
     x = tokens(12, 1024, "bf16").cuda()
