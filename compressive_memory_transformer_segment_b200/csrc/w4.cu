@@ -248,7 +248,9 @@ __device__ __forceinline__ void write_tile(const W4Problem& p, int tile, int t0,
 // memory by the lanes that will read them, so that they take no registers and
 // need no barrier.  (CTAs that stay and go on to further tiles with the ring
 // running on were slower: their addresses and bounds are more instructions than a new
-// CTA's; one token, 4096 -> 131072, 100 us against 84.)  NT: tiles of 8 tokens.
+// CTA's; one token, 4096 -> 131072, 100 us against 84.)  8 warps and three CTAs an SM:
+// one token, 4096 -> 16384, 13.2 us; 4 warps 14.2, two CTAs 15.3, four 14.3 (spills).
+// NT: tiles of 8 tokens.
 template <typename T, int NT, int NG>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1)
 w4_split_kernel(W4Problem p) {
