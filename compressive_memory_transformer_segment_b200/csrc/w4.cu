@@ -18,8 +18,9 @@
 // Layout (see the header): a row's 128-channel blocks are stored so that the
 // 16 bytes lane 4 i + c loads hold exactly the codes that lane's fragments
 // need (chunk c of the block: word j = channels 32 j + 8 c .. + 7), and the
-// same 8 channels of a token are 16 contiguous bytes.  So both operands go
-// from global memory to the tensor cores without shared memory or shuffles.
+// same 8 channels of a token are 16 contiguous bytes.  So no operand is shuffled
+// between lanes; shared memory only holds codes on their way (split) or the tokens
+// that four warps share (rows).
 //
 // A CTA takes 16 rows, whose blocks its 8 warps share out (their sums are added
 // in warp order through shared memory), or, for 9 tokens and more and where that
