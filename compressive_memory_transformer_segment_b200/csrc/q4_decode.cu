@@ -10,8 +10,7 @@
 // so both products run over the codes themselves on the tensor cores, with the
 // scales on the outside of the first and folded into the probabilities of the
 // second.  Queries and probabilities times scale meet the codes as fp16, in its
-// range by powers of two: one part for bf16 heads (2^-12 of a term, less than
-// their own rounding), two for fp32 heads (2^-23).
+// range by powers of two (see Attention).
 //
 // The floor is the buffer's bytes (5 bits per value), but what bounds it at 64
 // streams is the instructions around them: with 4 query heads per KV head half of
@@ -27,8 +26,8 @@
 // (no barrier), three tiles ahead.
 //
 // Measured (device time): 2 streams at the end of 2048-row segments, 32/8 heads of
-// 128, 13 us (6 MB: latency alone); 64 streams at ragged positions below 8192 105
-// us for 370 MB, 3.5 TB/s, 0.54 of the copy rate; 8 x 8 x 1500 rows appended and read
+// 128, 14 us (6 MB: latency alone); 64 streams at ragged positions below 8192 111
+// us for 370 MB, 3.3 TB/s, 0.51 of the copy rate; 8 x 8 x 1500 rows appended and read
 // back 34 us for 137 MB, 4.0 TB/s (bound by the instructions that choose the codes).
 //
 // Grid: the rows of all (stream, KV head, chunk of 8 query heads) are shared out
@@ -226,7 +225,7 @@ __device__ __forceinline__ void store_token(const Q4Problem& p, size_t bh, size_
                  (key ? p.k_scale : p.v_scale) + row * (D / 16), active);
 }
 
-// fp16 parts that hold a query or a probability of this type.
+// fp16 parts that hold a query of this type.
 template <typename T> struct Parts;
 template <> struct Parts<__nv_bfloat16> { static constexpr int n = 1; };
 template <> struct Parts<float> { static constexpr int n = 2; };
@@ -358,25 +357,6 @@ struct Ring {
       t.kcen[e] = __byte_perm(a, b, 0x5410);
     }
   }
-  // The largest scale of this lane's share of a slot's 16 rows of values, as bf16
-  // bits; FINITE: of those that are neither infinite nor NaN.
-  template <bool FINITE>
-  __device__ __forceinline__ uint32_t top_scale(int slot) const {
-    const uint8_t* s = smem + slot * kSlot + 2 * kCodes + kParams;
-    Raw<D / 16> half;  // half a row's parameters per lane
-    uint32_t top = 0;
-    const auto add = [&](uint32_t w) {
-      if (!FINITE || (w & 0x7f80u) != 0x7f80u) top = __vmaxu2(top, w);
-    };
-    if constexpr (D == 32) {
-      add(*reinterpret_cast<const uint32_t*>(s + (lane & 15) * 4));
-    } else {
-      half.load(s + lane * (D / 16));
-#pragma unroll
-      for (int j = 0; j < D / 64; ++j) add(half.word(j));
-    }
-    return top & 0xffffu;  // the scales are the low halves
-  }
   __device__ __forceinline__ void read(ValueTile<D>& t, int slot) const {
     const int i = lane >> 2, c = lane & 3, kr = k_row(i);
     const uint8_t* s = smem + slot * kSlot;
@@ -403,9 +383,12 @@ __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t (&out)[4]) {
   out[3] = (w >> 8) & 0x00f000f0u;
 }
 // The tensor cores align such products by their operands' exponents, zeros in
-// front included, which leaves about 2^-16 of a sum: right for bf16 heads, not
-// for fp32 ones.  Those take q - 8 as a normal number: 1024 + q by insertion,
-// minus 1032; 1024 + 16 q, over 16 and minus 72 (both exact).
+// front included, which drops what lies 2^-13 of a code below the largest product:
+// at most 2^-13 of the span of a sum's codes, and about 2^-16 of a sum of 16 terms
+// of a size.  That is right for bf16 heads, not for fp32 ones.  Those take q - 8 as a
+// normal number: 1024 + q by insertion, minus 1032; 1024 + 16 q, over 16 and minus
+// 72 (both exact).  (For bf16 heads the codes three bits further up, by one shift
+// more in two: 114.6 us against 111.3 for 64 streams.)
 template <bool EXACT>
 __device__ __forceinline__ void code_pairs(uint32_t w, uint32_t (&out)[4]) {
   codes_f16(w, out);
@@ -451,11 +434,22 @@ __device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
 
 // Running attention of one warp over its rows, for 8 heads: fragments of
-// heads 2c, 2c + 1.  The operands that meet the codes are fp16 (bf16 heads:
-// one part, 2^-12 of a term; fp32 heads: two, 2^-23), kept in its range by
-// powers of two: a head's query by its largest element, the probabilities
-// times scale by the largest scale seen.
-template <int D, int NP>
+// heads 2c, 2c + 1.  The operands that meet the codes are fp16.
+// Queries are kept in its range by a power of two per head, set by the largest
+// element: bf16 heads in one part (exact down to 2^-29 of that), fp32 heads in two
+// (2^-22 of an element, and 2^-40 of the largest).
+// The weights, probabilities times scale, go in as two parts (2^-22 of a weight, for
+// bf16 heads 2^-21): one part, 2^-11 at most, would be the sum's largest error, since it
+// counts by the codes, which all lie on one side of zero (bf16 heads, 2048 rows: 4e-4 of
+// the output against 2e-5).  With at most 4 query heads per KV head and one part per
+// query (kPaired) the second parts take the columns of heads 4 .. 7, whose lanes hold the
+// same four heads again: 64 streams 111 us, against 107 with one part and 125 with
+// two products.
+// The weights' range is a power of two for each head and group (`unit`): their largest
+// so far lies at 2^8 .. 2^15 (lower() and rebase() see to it), so that what fp16
+// drops, 2^-24, is 2^-32 of it or less, whatever the scales of other groups, of rows of
+// little probability, and of what other heads attend to.
+template <int D, int NP, bool WIDE>
 struct Attention {
   static constexpr int NJ = D / 32;
   static constexpr bool kExact = NP > 1;
@@ -463,6 +457,9 @@ struct Attention {
   static constexpr float kOdd = kExact ? 1.f : 0.0625f;          // second and fourth codes
   static constexpr float kCenter = kExact ? 8.f : 0.f;
   static constexpr float kLead = 7.f;
+  static constexpr bool kPaired = NP == 1 && !WIDE;
+  static constexpr int VP = kPaired ? 1 : 2;                     // parts of a weight in a lane
+  static constexpr float kMostUnit = 0x1p120f;
   uint32_t qf[NJ][NP][4];  // queries of head i as B fragments, times 2^e (pairs 1, 3: kOdd of that)
   // Sums of head i's scaled query over each group, in units of a code, as a B
   // operand of bf16 parts: index 4 part + group (d = 128), 2 part + group (64),
@@ -470,21 +467,22 @@ struct Attention {
   uint32_t qs[2], qc[2];   // (qc: times kCenter)
   float f1, f2[2];         // log2(e) / sqrt(d) kUnit1, 2^-e: scores to powers of two
   float m[2], l[2];        // reference of the powers; their sum over this lane's rows
-  float o[2 * NJ][4];      // O^T without the minima, times 2^-pe / kUnit1 (rows i + 8: over kOdd too)
-  float omin[NJ][2];       // sum of p (minimum + kCenter scale) over this lane's rows
-  int pe;                  // p scale 2^-pe is what the products get
-  uint32_t limit;          // bf16 bits of the largest scale that 2^-pe takes to 2^8
+  float o[2 * NJ][4];      // O^T without the minima, times unit / kUnit1 (rows i + 8: over kOdd too)
+  float2 omin[NJ];         // sum of p (minimum + kCenter scale) over this lane's rows
+  float2 unit[NJ];         // powers of two: p scale unit is what group j's products get
+  float minus;             // kPaired: 0 in the lanes of the first parts, -1 of the second
 
   // q_t: this KV head's first query; ng: heads of it that exist.
   template <typename T>
   __device__ __forceinline__ void init(const T* q_t, int ng, int lane) {
-    const int i = lane >> 2, c = lane & 3;
+    const int i = lane >> 2, c = lane & 3, head = kPaired ? i & 3 : i;
+    minus = c < 2 ? 0.f : -1.f;
     float x[NJ][8], top = 0.f;
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[j][e] = 0.f;
-      if (i < ng) load8(q_t + (size_t)i * D + 32 * j + 8 * c, x[j]);
+      if (head < ng) load8(q_t + (size_t)head * D + 32 * j + 8 * c, x[j]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[j][e]));
     }
@@ -546,47 +544,66 @@ struct Attention {
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      omin[j][0] = omin[j][1] = 0.f;
+      omin[j] = both<float2>(0.f);
+      unit[j] = both<float2>(kMostUnit);
 #pragma unroll
       for (int k = 0; k < 4; ++k) o[2 * j][k] = o[2 * j + 1][k] = 0.f;
     }
     m[0] = m[1] = -INFINITY;
     l[0] = l[1] = 0.f;
-    pe = -120;
-    limit = 0;
   }
 
-  // The reference becomes the maximum so far.
+  // 1 / x of a power of two, 2^-126 <= x <= 2^126.
+  __device__ __forceinline__ static float inverse(float x) { return __int_as_float((254 << 23) - __float_as_int(x)); }
+  // O^T of group j and head h, times x.
+  __device__ __forceinline__ void scale_o(int j, int h, float x) {
+    o[2 * j][h] *= x; o[2 * j][2 + h] *= x;
+    o[2 * j + 1][h] *= x; o[2 * j + 1][2 + h] *= x;
+  }
+
+  // The reference becomes the maximum so far.  The weights that were the largest
+  // are now smaller by the factor corr: the units grow by the power of two below 1 / corr.
   __device__ __forceinline__ void rebase(float top0, float top1) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const float mn = fmaxf(m[h], column_max(h ? top1 : top0));
       const float corr = exp2_approx(m[h] - mn);  // 0 for the first rows
+      const float grow = pow2((int)fminf(mn - m[h], 126.f));
       m[h] = mn;
       l[h] *= corr;
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
-        omin[j][h] *= corr;
-        o[2 * j][h] *= corr; o[2 * j][2 + h] *= corr;
-        o[2 * j + 1][h] *= corr; o[2 * j + 1][2 + h] *= corr;
+        float& u = h ? unit[j].y : unit[j].x;
+        float& om = h ? omin[j].y : omin[j].x;
+        const float to = fminf(u * grow, kMostUnit);
+        om *= corr;
+        scale_o(j, h, corr * (to * inverse(u)));
+        u = to;
       }
     }
   }
 
-  // A scale beyond the limit: the unit moves so that the largest of these rows
-  // lies at 1 .. 2 (the first rows set it so).  With probabilities up to
-  // 2^kLead there is room for scales 2^7 times as large before the next move.
-  __device__ __forceinline__ void raise(uint32_t top) {
-    top = __reduce_max_sync(0xffffffffu, top);
-    if (top <= limit) return;
-    const int to = max(min((int)(top >> 7) - 127, 126), -120);
-    const float down = exp2f((float)(pe - to));
+  // A weight of this tile reached 2^15 (the first rows' do, but for scales next to 0):
+  // the unit of its head and group moves so that the largest lies at 2^8 .. 2^9.
+  __device__ __forceinline__ void lower(const ValueTile<D>& t, const float (&pr)[4]) {
 #pragma unroll
-    for (int j = 0; j < 2 * NJ; ++j)
+    for (int j = 0; j < NJ; ++j)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[j][e] *= down;
-    pe = to;
-    limit = min(to + 8 + 127, 255) << 7;
+      for (int h = 0; h < 2; ++h) {
+        float top = 0.f;  // the largest over 2^8: no product of finite values is infinite
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float w = (pr[2 * e + h] * 0x1p-8f) * t.vp[e].scale(j);
+          top = fmaxf(top, w < INFINITY ? w : 0.f);  // (a lost group or score has no say)
+        }
+        top = column_max(top);
+        float& u = h ? unit[j].y : unit[j].x;
+        if (top * 0x1p-7f * u >= 1.f) {
+          const float to = pow2(127 - (__float_as_int(top) >> 23));
+          scale_o(j, h, to * inverse(u));
+          u = to;
+        }
+      }
   }
 
   // Scores (as powers of two) of rows k_row(i) (x[0], x[1]) and + 8 (x[2],
@@ -620,12 +637,38 @@ struct Attention {
     for (int e = 0; e < 4; ++e) x[e] = kr + 8 * (e >> 1) < left ? s[e] * f1 * f2[e & 1] : -INFINITY;
   }
 
+  // A tile's weights p scale unit as fp16 parts: [group][rows k_row(i), + 8][part].
+  __device__ __forceinline__ void weigh(const ValueTile<D>& t, const float (&pr)[4], uint32_t (&w)[NJ][2][VP]) const {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float sc = t.vp[e].scale(j);
+        float2 x = mul(mul({pr[2 * e], pr[2 * e + 1]}, unit[j]), {sc, sc});
+        if constexpr (kPaired) {
+          // The leading 11 bits (which is what truncating to fp16 leaves), or the rest.
+          const float2 lead = {__uint_as_float(__float_as_uint(x.x) & 0xffffe000u),
+                               __uint_as_float(__float_as_uint(x.y) & 0xffffe000u)};
+          x = fma(lead, {minus, minus}, x);
+          asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(w[j][e][0]) : "f"(x.y), "f"(x.x));
+        } else {
+#pragma unroll
+          for (int part = 0; part < VP; ++part) w[j][e][part] = split_f16(x.x, x.y);
+        }
+      }
+  }
+
   // O^T += V^T P^T of a tile with probabilities pr.
   __device__ __forceinline__ void values(const ValueTile<D>& t, const float (&pr)[4]) {
-    const float p2 = pow2(-pe);
-    float w[4];
+    uint32_t w[NJ][2][VP];
+    weigh(t, pr, w);
+    uint32_t top = 0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) w[e] = pr[e] * p2;
+    for (int j = 0; j < NJ; ++j) top = __vmaxu2(top, __vmaxu2(w[j][0][0], w[j][1][0]));
+    if (__builtin_expect(__any_sync(0xffffffffu, max(top & 0xffffu, top >> 16) >= 0x7800u), 0)) {
+      lower(t, pr);
+      weigh(t, pr, w);
+    }
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
       // Codes of group j: element t of a lane's four is channel 32 j + 4 i + t,
@@ -633,20 +676,15 @@ struct Attention {
       uint32_t lo[4], hi[4];
       code_pairs<kExact>(t.v[0].half_pair(t.v[1], j), lo);
       code_pairs<kExact>(t.v[2].half_pair(t.v[3], j), hi);
-      float ws[4];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const float sc = t.vp[e].scale(j);
         const float mn = kExact ? fmaf(kCenter, sc, t.vp[e].minimum(j)) : t.vp[e].minimum(j);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          ws[2 * e + h] = w[2 * e + h] * sc;
-          omin[j][h] = fmaf(pr[2 * e + h], mn, omin[j][h]);
-        }
+        omin[j] = fma({pr[2 * e], pr[2 * e + 1]}, {mn, mn}, omin[j]);
       }
 #pragma unroll
-      for (int part = 0; part < NP; ++part) {
-        const uint32_t b0 = transpose8(split_f16(ws[0], ws[1])), b1 = transpose8(split_f16(ws[2], ws[3]));
+      for (int part = 0; part < VP; ++part) {
+        const uint32_t b0 = transpose8(w[j][0][part]), b1 = transpose8(w[j][1][part]);
         mma_f16(o[2 * j], lo[0], lo[1], hi[0], hi[1], b0, b1);
         mma_f16(o[2 * j + 1], lo[2], lo[3], hi[2], hi[3], b0, b1);
       }
@@ -654,17 +692,11 @@ struct Attention {
   }
 
   // Probabilities (powers of two relative to a reference m, at most 2^kLead) of
-  // a tile from its scores x; the tile lies in `slot`.  A maximum is taken over the warp only when a score leaves that
-  // room (and by the first rows), not for every tile.
-  __device__ __forceinline__ void probabilities(const float (&x)[4], const Ring<D>& ring, int slot,
-                                                float (&pr)[4]) {
+  // a tile from its scores x.  A maximum is taken over the warp only when a score
+  // leaves that room (and by the first rows), not for every tile.
+  __device__ __forceinline__ void probabilities(const float (&x)[4], float (&pr)[4]) {
     const float top0 = fmaxf(x[0], x[2]), top1 = fmaxf(x[1], x[3]);
-    if (__builtin_expect(__any_sync(0xffffffffu, fmaxf(top0 - m[0], top1 - m[1]) > kLead ||
-                                                    ring.template top_scale<false>(slot) > limit), 0)) {
-      rebase(top0, top1);
-      // (A group whose scale is NaN or infinite has no say in the others' unit.)
-      raise(ring.template top_scale<true>(slot));
-    }
+    if (__builtin_expect(__any_sync(0xffffffffu, fmaxf(top0 - m[0], top1 - m[1]) > kLead), 0)) rebase(top0, top1);
 #pragma unroll
     for (int e = 0; e < 4; ++e) pr[e] = exp2_approx(x[e] - m[e & 1]);
     l[0] += pr[0] + pr[2];
@@ -696,7 +728,7 @@ struct Attention {
         __syncwarp();  // every lane has read the slot
       }
       ring.next(before, x + R::kStages - 1);
-      probabilities(s, ring, slot, pr);
+      probabilities(s, pr);
       before = slot;
       slot = slot + 1 < R::kStages ? slot + 1 : 0;
     }
@@ -943,7 +975,7 @@ template <int D> constexpr int kSumBytes = kWarps * kHeads * (D + 2) * 4;
 template <int D> constexpr int kNumBytes = kWarps * kHeads * D * 4;
 template <int D> constexpr int kSmemBytes = kRingBytes<D> + kSumBytes<D> + kNumBytes<D>;
 
-template <typename T, int D>
+template <typename T, int D, bool WIDE>
 __global__ void __launch_bounds__(kThreads, Parts<T>::n == 1 ? kResident : 2)
 q4_decode_kernel(Q4Problem p) {
   static_assert(kThreads == 16 * kHeads, "16 threads a head");
@@ -972,7 +1004,7 @@ q4_decode_kernel(Q4Problem p) {
   const uint32_t u_end = share.first(blockIdx.x + 1);
   run.end = share.first(blockIdx.x);
   R ring;
-  Attention<D, NP> at;
+  Attention<D, NP, WIDE> at;
   float den = 0.f;  // sigma(q) z over the run's rows of M, of head threadIdx.x / 16
   at.clear();
 #pragma unroll 1
@@ -1035,7 +1067,6 @@ q4_decode_kernel(Q4Problem p) {
       if (threadIdx.x % 16 == 0 && (int)threadIdx.x / 16 < done.ng) part[threadIdx.x / 16].den = den;
       __syncthreads();  // sigma(q) has been read
       // This warp's (max, sum, acc) of heads 2c, 2c + 1.
-      const float unit = exp2f((float)at.pe);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         at.l[h] = column_sum(at.l[h]);
@@ -1045,10 +1076,15 @@ q4_decode_kernel(Q4Problem p) {
         }
 #pragma unroll
         for (int j = 0; j < D / 32; ++j) {
-          const float add = column_sum(at.omin[j][h]);
+          const float add = column_sum(h ? at.omin[j].y : at.omin[j].x);
+          const float unit = at.inverse(h ? at.unit[j].y : at.unit[j].x);
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             float* to = &red[warp][2 * c + h][32 * j + 4 * i + 2 * k];
+            if constexpr (Attention<D, NP, WIDE>::kPaired) {
+              at.o[2 * j + k][h] += __shfl_xor_sync(0xffffffffu, at.o[2 * j + k][h], 2);
+              at.o[2 * j + k][2 + h] += __shfl_xor_sync(0xffffffffu, at.o[2 * j + k][2 + h], 2);
+            }
             to[0] = at.o[2 * j + k][h] * at.kUnit1 * unit + add;
             to[1] = at.o[2 * j + k][2 + h] * (at.kUnit1 * at.kOdd) * unit + add;
           }
@@ -1222,9 +1258,13 @@ cudaError_t launch(const Q4Problem& p, Q4What what, int n, void* k, void* v, cud
   switch (what) {
     case Q4What::kStep: {
       constexpr int bytes = kSmemBytes<D>;
+      // WIDE: the second parts of the weights find no free columns (fp32 heads always take
+      // products of their own, next to those of the queries' two parts).
+      constexpr bool kAlways = Parts<T>::n > 1;
+      auto* kernel = kAlways || p.H_q / p.H_kv > kHeads / 2 ? q4_decode_kernel<T, D, true>
+                                                            : q4_decode_kernel<T, D, kAlways>;
       if (bytes > 48 * 1024) {
-        cudaError_t e =
-            cudaFuncSetAttribute(q4_decode_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) return e;
       }
       const Q4Plan plan = q4_plan(p.B, p.H_q, p.H_kv, p.S);
@@ -1232,7 +1272,7 @@ cudaError_t launch(const Q4Problem& p, Q4What what, int n, void* k, void* v, cud
       q.ctas = (int)plan.ctas;
       q.unit = plan.unit;
       q.lead = plan.lead;
-      q4_decode_kernel<T, D><<<(unsigned)plan.ctas, kThreads, bytes, st>>>(q);
+      kernel<<<(unsigned)plan.ctas, kThreads, bytes, st>>>(q);
       break;
     }
     case Q4What::kAppend: q4_append_kernel<T, D><<<rows, kMoveThreads, 0, st>>>(p, n); break;
