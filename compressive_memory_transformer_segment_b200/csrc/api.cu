@@ -1068,19 +1068,24 @@ Q4Problem q4_problem(const infini_dims_t* d, int seg_len, const CacheQ4& c) {
   return p;
 }
 
-// Workspace of a 4-bit decode step: [tickets | partials].
+// Workspace of a 4-bit decode step: [tickets | partials].  The tickets have room for
+// every shape, so that no shape's partials lie where another has its tickets: one
+// workspace, zeroed once, serves them all.
+constexpr long long kQ4MostHeads = 65535;  // B * H_q
+const size_t kQ4TicketBytes = align_up(kQ4MostHeads * 4);
+
 struct Q4Layout {
-  size_t part, total;
+  size_t tickets, total;  // bytes of the tickets in use, of all
 };
 
 int q4_layout(const infini_dims_t* d, int seg_len, Q4Layout* lay) {
   if (!d || d->B < 1 || d->H_q < 1 || d->H_kv < 1 || seg_len < 1 || d->H_q % d->H_kv != 0)
     return INFINI_ERR_ARG;
-  if (d->d_k != d->d_v || !head_dim_ok(d->d_k) || (long long)d->B * d->H_q > 65535 || seg_len > (1 << 30))
+  if (d->d_k != d->d_v || !head_dim_ok(d->d_k) || (long long)d->B * d->H_q > kQ4MostHeads || seg_len > (1 << 30))
     return INFINI_ERR_UNSUPPORTED;
   const int zc = q4_head_chunks(d->H_q / d->H_kv);
-  lay->part = align_up((size_t)d->B * d->H_kv * zc * 4);
-  lay->total = align_up(lay->part + q4_partial_bytes(d->B, d->H_q, d->H_kv, seg_len, d->d_k));
+  lay->tickets = (size_t)d->B * d->H_kv * zc * 4;  // (at most one for each query head)
+  lay->total = align_up(kQ4TicketBytes + q4_partial_bytes(d->B, d->H_q, d->H_kv, seg_len, d->d_k));
   return INFINI_OK;
 }
 
@@ -1231,14 +1236,14 @@ int infini_attn_decode_step_q4(const void* q_t, const void* k_t, const void* v_t
   if (!ws) {
     if (cudaMallocAsync(reinterpret_cast<void**>(&ws), lay.total, st) != cudaSuccess) return INFINI_ERR_CUDA;
     owned = true;
-    if (cudaMemsetAsync(ws, 0, lay.part, st) != cudaSuccess) {
+    if (cudaMemsetAsync(ws, 0, lay.tickets, st) != cudaSuccess) {
       cudaFreeAsync(ws, st);
       return INFINI_ERR_CUDA;
     }
   }
   p.q_t = q_t; p.k_t = k_t; p.v_t = v_t; p.beta = beta; p.pos = pos; p.M = M; p.z = z; p.out_t = out_t;
   p.ctr = reinterpret_cast<unsigned int*>(ws);
-  p.part = reinterpret_cast<float*>(ws + lay.part);
+  p.part = reinterpret_cast<float*>(ws + kQ4TicketBytes);
   cudaError_t e = launch_q4(p, Q4What::kStep, 1, nullptr, nullptr, st);
   if (owned) {
     cudaError_t f = cudaFreeAsync(ws, st);

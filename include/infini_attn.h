@@ -550,7 +550,8 @@ INFINI_API int infini_attn_state_update_q4(const infini_cache_q4_t* cache, const
 /* Bytes of device workspace infini_attn_decode_step_q4 needs (0 if the sizes
  * are invalid; dims->L is ignored).  Like infini_attn_decode_step's it must be
  * zero-filled before its first step and serves one call at a time: calls that
- * may run at the same time (two streams, two captured graphs) need one each. */
+ * may run at the same time (two streams, two captured graphs) need one each.
+ * Steps of different sizes may share one that is large enough for each of them. */
 INFINI_API size_t infini_attn_decode_q4_workspace_bytes(const infini_dims_t* dims, int seg_len);
 
 /* One decode step over a 4-bit segment buffer, every stream at its own
