@@ -556,10 +556,14 @@ int row_grid(long long rows, const Shape& s) {
   return (int)(rows < most ? rows : most);
 }
 
-template <typename K>
+// The limit of a kernel's shared memory belongs to the kernel, not to the call: it is set
+// to the most that any width asks of this instance (PIECE: a thread's bytes of a row), the
+// same value by every host thread.
+template <int PIECE, bool COPIES, typename K>
 cudaError_t run(K kernel, const BlockNormProblem& p, const Shape& s, cudaStream_t st) {
-  if (s.smem + 1024 > 48 * 1024) {  // (some of the default is the sums')
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s.smem);
+  constexpr int stages = stages_of(PIECE, COPIES), most = stages > 1 ? PIECE * kMaxThreads * stages : 0;
+  if (most + 1024 > 48 * 1024) {  // (some of the default is the sums')
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return e;
   }
   kernel<<<row_grid(p.rows, s), s.threads, s.smem, st>>>(p);
@@ -568,8 +572,9 @@ cudaError_t run(K kernel, const BlockNormProblem& p, const Shape& s, cudaStream_
 
 template <bool BWD, typename T, int V, int N>
 cudaError_t launch_n(const BlockNormProblem& p, const Shape& s, cudaStream_t st) {
-  if constexpr (BWD) return run(block_norm_bwd_kernel<T, V, N>, p, s, st);
-  else return run(block_norm_fwd_kernel<T, V, N>, p, s, st);
+  constexpr int bytes = V * (int)sizeof(T);
+  if constexpr (BWD) return run<5 * N * bytes, bytes >= 4>(block_norm_bwd_kernel<T, V, N>, p, s, st);
+  else return run<3 * N * bytes, bytes >= 4>(block_norm_fwd_kernel<T, V, N>, p, s, st);
 }
 
 template <bool BWD, typename T, int V>
