@@ -452,16 +452,22 @@ block_norm_bwd_kernel(BlockNormProblem p) {
           for (int e = 0; e < W; ++e) f[i][e] = both<L>(0.f);
         }
       }
-      float m = 0.f;
-      if (p.w_post) m = block_sum(sum(dot), slots, turn) * inv_d;
+      if (p.w_post) {
+        const float m = block_sum(sum(dot), slots, turn) * inv_d;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+          for (int e = 0; e < W; ++e)
+            f[i][e] = mul(both<L>(rp), fma(mul(raw[3][i].get(e), both<L>(rp)), both<L>(-m), f[i][e]));
+      }
+      // (Without the norm do does not depend on o: f, and not f - o 0, NaN for an infinite o.)
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const int v = threadIdx.x + i * blockDim.x;
         if (v < nvec) {
           typename S::P out;
 #pragma unroll
-          for (int e = 0; e < W; ++e)
-            out.set(e, mul(both<L>(rp), fma(mul(raw[3][i].get(e), both<L>(rp)), both<L>(-m), f[i][e])));
+          for (int e = 0; e < W; ++e) out.set(e, f[i][e]);
           out.store(p.d_o, here + (size_t)i * blockDim.x * V);
         }
       }

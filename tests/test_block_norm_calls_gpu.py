@@ -44,3 +44,25 @@ def test_host_threads_with_different_widths(cuda_lib):
         t.join()
     torch.cuda.synchronize()
     assert refused == [0] * len(work)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("next_norm", [False, True])
+def test_gradient_of_an_infinite_output_without_its_norm(cuda_lib, next_norm, dtype):
+    """Without w_post, do = G scale sg(gate) does not depend on o: it is finite where o
+    is infinite or NaN.  Against the call with a finite o: the same bits."""
+    rows, width = 5, 264
+    o = randn(rows, width, seed=1, dtype=dtype)
+    lost = o.clone()
+    lost[0, 3], lost[1, 200], lost[4, 263] = float("inf"), float("nan"), -float("inf")
+    args = (randn(rows, width, seed=2, dtype=dtype), randn(rows, width, seed=3, dtype=dtype) if next_norm else None,
+            randn(rows, width, seed=4, dtype=dtype) if next_norm else None,
+            randn(rows, seed=5).abs() + 1 if next_norm else None, randn(width, seed=6) if next_norm else None)
+    more = dict(gate=randn(rows, width, seed=7, dtype=dtype), scale=randn(width, seed=8))
+    want = cuda_lib.block_norm_backward(*args, o=o, **more)
+    got = cuda_lib.block_norm_backward(*args, o=lost, **more)
+    assert torch.isfinite(want.do).all() and torch.equal(got.do, want.do) and torch.equal(got.dr, want.dr)
+    here = ~torch.isfinite(lost)
+    assert not torch.isfinite(got.dgate[here]).any() and torch.equal(got.dgate[~here], want.dgate[~here])
+    plain = (~here).all(0)
+    assert not torch.isfinite(got.dscale[~plain]).any() and torch.equal(got.dscale[plain], want.dscale[plain])
