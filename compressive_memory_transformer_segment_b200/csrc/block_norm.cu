@@ -222,19 +222,35 @@ __device__ __forceinline__ float rcp(float x) {
   asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(x));
   return x;
 }
+__device__ __forceinline__ float ex2_lanes(float x) { return ex2(x); }
+__device__ __forceinline__ float2 ex2_lanes(float2 x) { return {ex2(x.x), ex2(x.y)}; }
+__device__ __forceinline__ float rcp_lanes(float x) { return rcp(x); }
+__device__ __forceinline__ float2 rcp_lanes(float2 x) { return {rcp(x.x), rcp(x.y)}; }
+__device__ __forceinline__ float most(float x, float y) { return fmaxf(x, y); }
+__device__ __forceinline__ float2 most(float2 x, float y) { return {fmaxf(x.x, y), fmaxf(x.y, y)}; }
+__device__ __forceinline__ float least(float x, float y) { return fminf(x, y); }
+__device__ __forceinline__ float2 least(float2 x, float y) { return {fminf(x.x, y), fminf(x.y, y)}; }
+
 // Logistic of a gate logit, u, and 1 - u (as e^-a u, which keeps its digits
-// where u rounds to 1), by the hardware's approximations of 2^x and 1 / x
-// (relative error 2^-21 together).  0 and 1 in the limits, NaN for NaN; the bound only
-// keeps infinity times 0 out of 1 - u, where u is 0 and wanted as such.
-__device__ __forceinline__ float sigmoid(float a, float& rest) {
-  const float t = ex2(a * -1.4426950408889634f), u = rcp(1.f + t);
-  rest = fminf(t, 1e30f) * u;
-  return u;
-}
-__device__ __forceinline__ float2 sigmoid(float2 a, float2& rest) {
-  a = mul(a, both<float2>(-1.4426950408889634f));
-  const float2 t = {ex2(a.x), ex2(a.y)}, s = add(t, both<float2>(1.f)), u = {rcp(s.x), rcp(s.y)};
-  rest = mul(float2{fminf(t.x, 1e30f), fminf(t.y, 1e30f)}, u);
+// where u rounds to 1), by the hardware's approximations of 2^x (2^-22) and 1 / x (2^-23).
+// 0 and 1 in the limits, NaN for NaN.  u is 0 from e^-a = 2^126 on, where 1 / x would be
+// subnormal, and 1 - u is then wanted times u only; the bound keeps infinity times 0 out of it.
+// The product a log2(e) is rounded to fp32, which e^-a feels |a| 2^-24 of: within 2^-17.5
+// up to |a| = 88, little beside bf16's 2^-8.  EXACT (fp32 rows) puts its remainder back
+// and keeps u to 2^-20.8 and 1 - u to 2^-20.
+template <bool EXACT, typename L>
+__device__ __forceinline__ L sigmoid(L a, L& rest) {
+  const L y = mul(a, both<L>(-1.4426950408889634f));
+  L t = ex2_lanes(y);
+  if constexpr (EXACT) {
+    // What the rounding of y and of log2(e) left, times ln 2.  (NaN or infinite where a or y
+    // is infinite: some factor then that leaves 0 and infinity what they are.)
+    const L left = fma(a, both<L>(-1.4426950408889634f), mul(y, both<L>(-1.f)));
+    const L e = mul(fma(a, both<L>(-1.9259629911266175e-8f), left), both<L>(0.6931471805599453f));
+    t = mul(t, add(least(most(e, -0.5f), 0.5f), both<L>(1.f)));
+  }
+  const L u = rcp_lanes(add(t, both<L>(1.f)));
+  rest = mul(least(t, 0x1p126f), u);
   return u;
 }
 
@@ -314,7 +330,7 @@ block_norm_fwd_kernel(BlockNormProblem p) {
           for (int e = 0; e < W; ++e) {
             L rest;
             const L n = mul(raw[1][i].get(e), both<L>(rp));
-            x[i][e] = fma(n, p.gate ? mul(sigmoid(raw[2][i].get(e), rest), c[e]) : c[e], x[i][e]);
+            x[i][e] = fma(n, p.gate ? mul(sigmoid<sizeof(T) == 4>(raw[2][i].get(e), rest), c[e]) : c[e], x[i][e]);
             out.set(e, x[i][e]);
           }
           out.store(p.r_out, here + (size_t)i * blockDim.x * V);
@@ -438,7 +454,7 @@ block_norm_bwd_kernel(BlockNormProblem p) {
 #pragma unroll
           for (int e = 0; e < W; ++e) {
             L rest = both<L>(0.f), gu = G[i][e];
-            if (p.gate) gu = mul(gu, sigmoid(raw[4][i].get(e), rest));
+            if (p.gate) gu = mul(gu, sigmoid<sizeof(T) == 4>(raw[4][i].get(e), rest));
             const L n = mul(raw[3][i].get(e), both<L>(rp));
             acc_a[i][e] = fma(gu, n, acc_a[i][e]);
             f[i][e] = mul(gu, c[e]);

@@ -66,3 +66,35 @@ def test_gradient_of_an_infinite_output_without_its_norm(cuda_lib, next_norm, dt
     assert not torch.isfinite(got.dgate[here]).any() and torch.equal(got.dgate[~here], want.dgate[~here])
     plain = (~here).all(0)
     assert not torch.isfinite(got.dscale[~plain]).any() and torch.equal(got.dscale[plain], want.dscale[plain])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_gates_of_every_size(cuda_lib, dtype):
+    """Logits over -87 .. 87, where neither the logistic u nor u (1 - u) is subnormal.
+    2^x is right to 2^-22, its argument's remainder adds two roundings, 2^-23, so t =
+    e^-a to 1.5 2^-22; 1 + t and 1 / x: u to 2.25 2^-22; 1 - u = t u to 4 2^-22; three
+    products: u (1 - u) to 7 2^-22.  bf16 rows leave the remainder out: |a| 2^-24 more of t, 2^-17.5 at
+    87, once in u and twice in 1 - u; and half a step of the type."""
+    left = 0.0 if dtype == "f32" else 2.0 ** -17.5
+    half = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -24
+    for width in (4096, 1019):  # pieces of 16 bytes, and single elements
+        a = torch.linspace(-87, 87, 3 * width, dtype=torch.float64).to(DT[dtype]).view(3, width).cuda()
+        one, zero = torch.ones_like(a), torch.zeros_like(a)
+        e = torch.exp(-a.double().abs())
+        u, du = torch.where(a > 0, 1 / (1 + e), e / (1 + e)), e / (1 + e) ** 2
+        r_out = cuda_lib.block_norm(zero, None, 1e-6, o=one, gate=a)[0]
+        g = cuda_lib.block_norm_backward(one, None, None, None, None, o=one, gate=a)
+        for got, want, bound in ((r_out, u, 2.25 * 2.0 ** -22 + left), (g.do, u, 2.25 * 2.0 ** -22 + left),
+                                 (g.dgate, du, 7 * 2.0 ** -22 + 3 * left)):
+            off = ((got.double() - want).abs() / want).max()
+            assert off <= (bound + half) * (1 + 2.0 ** -7), (float(off), bound)
+    # the limits
+    a = torch.tensor([[float("inf"), -float("inf"), float("nan"), 300.0, -300.0, 3e38, -3e38, 0.0]], dtype=DT[dtype]).cuda()
+    one, zero = torch.ones_like(a), torch.zeros_like(a)
+    r_out = cuda_lib.block_norm(zero, None, 1e-6, o=one, gate=a)[0]
+    g = cuda_lib.block_norm_backward(one, None, None, None, None, o=one, gate=a)
+    nan = float("nan")
+    for got, want in ((r_out, [1, 0, nan, 1, 0, 1, 0, 0.5]), (g.do, [1, 0, nan, 1, 0, 1, 0, 0.5]),
+                      (g.dgate, [0, 0, nan, 0, 0, 0, 0, 0.25])):
+        want = torch.tensor([want], dtype=DT[dtype]).cuda()
+        assert torch.allclose(got, want, rtol=2.0 ** -7, atol=0, equal_nan=True), (got, want)
