@@ -802,7 +802,8 @@ class CacheQ4:
                    torch.zeros(scale, dtype=torch.bfloat16, device=device))
 
     def row(self, b):
-        """Batch row b alone, as a view."""
+        """Batch row b alone, as a view, for append, read and state_update (the decode
+        step takes whole buffers)."""
         return CacheQ4(*(t[b:b + 1] for t in self.tensors))
 
     def _dims_ref(self, H_q, L, dtype):

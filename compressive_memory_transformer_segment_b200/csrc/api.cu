@@ -1037,8 +1037,10 @@ struct CacheQ4 {
   Range r[4];
 };
 
-// Sizes and pointers shared by the calls on a 4-bit segment buffer.
-int q4_shape(const infini_dims_t* d, int seg_len, const infini_cache_q4_t* cache, CacheQ4* c) {
+// Sizes and pointers shared by the calls on a 4-bit segment buffer.  `part`: the call takes
+// one batch row's part of larger arrays too, whose scales lie at a multiple of a row's
+// d / 8 bytes.
+int q4_shape(const infini_dims_t* d, int seg_len, const infini_cache_q4_t* cache, bool part, CacheQ4* c) {
   if (!d || d->B < 1 || d->H_kv < 1 || seg_len < 1) return INFINI_ERR_ARG;
   if (d->dtype != INFINI_DTYPE_BF16 && d->dtype != INFINI_DTYPE_F32) return INFINI_ERR_ARG;
   if (d->d_k != d->d_v || !head_dim_ok(d->d_k) || (long long)d->B * d->H_kv > 65535 || seg_len > (1 << 30))
@@ -1048,7 +1050,8 @@ int q4_shape(const infini_dims_t* d, int seg_len, const infini_cache_q4_t* cache
   const size_t codes = rows * (d->d_k / 2), scale = rows * (d->d_k / 32) * 4;
   void* const ptrs[] = {cache->k_codes, cache->k_scale, cache->v_codes, cache->v_scale};
   for (int i = 0; i < 4; ++i) {
-    if (!aligned16(ptrs[i])) return INFINI_ERR_ALIGN;
+    const uintptr_t align = part && i % 2 == 1 ? d->d_k / 8 : 16;
+    if (((uintptr_t)ptrs[i] & (align - 1)) != 0) return INFINI_ERR_ALIGN;
     c->r[i] = rng(ptrs[i], i % 2 == 0 ? codes : scale);
     for (int j = 0; j < i; ++j)
       if (overlap(c->r[i], c->r[j])) return INFINI_ERR_ALIAS;
@@ -1094,13 +1097,11 @@ int q4_layout(const infini_dims_t* d, int seg_len, Q4Layout* lay) {
 int infini_attn_cache_q4_append(const void* k, const void* v, const int* pos, const infini_dims_t* dims,
                                 int seg_len, const infini_cache_q4_t* cache, void* stream) {
   CacheQ4 c;
-  int rc = q4_shape(dims, seg_len, cache, &c);
+  int rc = q4_shape(dims, seg_len, cache, true, &c);
   if (rc != INFINI_OK) return rc;
   if (!k || !v || !pos || dims->L < 1) return INFINI_ERR_ARG;
   if (dims->L > seg_len) return INFINI_ERR_ARG;
-  const void* ptrs[] = {k, v, pos};
-  for (const void* p : ptrs)
-    if (!aligned16(p)) return INFINI_ERR_ALIGN;
+  if (!aligned16(k) || !aligned16(v) || ((uintptr_t)pos & 3u) != 0) return INFINI_ERR_ALIGN;
   const size_t n = (size_t)dims->B * dims->H_kv * dims->L * dims->d_k *
                    (dims->dtype == INFINI_DTYPE_BF16 ? 2 : 4);
   const Range ins[] = {rng(k, n), rng(v, n), rng(pos, (size_t)dims->B * 4)};
@@ -1120,7 +1121,7 @@ int infini_attn_cache_q4_append(const void* k, const void* v, const int* pos, co
 int infini_attn_cache_q4_read(const infini_cache_q4_t* cache, const infini_dims_t* dims, int seg_len,
                               void* k, void* v, void* stream) {
   CacheQ4 c;
-  int rc = q4_shape(dims, seg_len, cache, &c);
+  int rc = q4_shape(dims, seg_len, cache, true, &c);
   if (rc != INFINI_OK) return rc;
   if (!k || !v || dims->L < 1 || dims->L > seg_len) return INFINI_ERR_ARG;
   if (!aligned16(k) || !aligned16(v)) return INFINI_ERR_ALIGN;
@@ -1148,7 +1149,7 @@ int infini_attn_state_update_q4(const infini_cache_q4_t* cache, const float* M_i
                                 int rule, const infini_dims_t* dims, int seg_len, float* M_out,
                                 float* z_out, void* workspace, size_t workspace_bytes, void* stream) {
   CacheQ4 c;
-  int rc = q4_shape(dims, seg_len, cache, &c);
+  int rc = q4_shape(dims, seg_len, cache, true, &c);
   if (rc != INFINI_OK) return rc;
   if (!M_in || !z_in || !M_out || !z_out || dims->L < 1 || dims->L > seg_len) return INFINI_ERR_ARG;
   Shape s;
@@ -1205,7 +1206,7 @@ int infini_attn_decode_step_q4(const void* q_t, const void* k_t, const void* v_t
   Q4Layout lay;
   CacheQ4 c;
   int rc = q4_layout(dims, seg_len, &lay);
-  if (rc == INFINI_OK) rc = q4_shape(dims, seg_len, cache, &c);
+  if (rc == INFINI_OK) rc = q4_shape(dims, seg_len, cache, false, &c);
   if (rc != INFINI_OK) return rc;
   if (!q_t || !k_t || !v_t || !beta || !pos || !M || !z || !out_t) return INFINI_ERR_ARG;
   const void* ptrs[] = {q_t, k_t, v_t, beta, pos, M, z, out_t};

@@ -505,8 +505,11 @@ INFINI_API int infini_attn_decode_step(const void* q_t, const void* k_t, const v
  * All little-endian.  The calls below take dims with B, H_kv, d_k = d_v = d in
  * {32, 64, 128} and dtype (the element type of the rows given or returned),
  * seg_len <= 2^30, B * H_q <= 65535, four arrays that do not overlap, 16-byte
- * aligned.  Rows that a call does not write keep what they hold, and rows
- * behind a stream's last one are never read. */
+ * aligned.  Append, read and state update also take one batch row's part of
+ * larger arrays (B = 1): the scales need d / 8 bytes' alignment there, which every
+ * row has, and pos 4 bytes'; the decode step takes whole arrays.  Rows that a call
+ * does not write keep what they hold, and rows behind a stream's last one are
+ * never read. */
 typedef struct {
   void* k_codes;
   void* k_scale;
