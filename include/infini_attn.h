@@ -323,7 +323,8 @@ INFINI_API int infini_attn_w4_dequantize(const void* packed, const void* scales,
                                          int N, int K, int group, int dtype, void* w, void* stream);
 
 /* y[t] = W x[t] + bias for M tokens, W in 4 bits as above:
- *   x          device [M, K], element type dtype (finite)
+ *   x          device [M, K], element type dtype (finite; the sum of (q - zero) x
+ *              over a group must lie within fp32, as it does for |x| < 1e35)
  *   bias       device float32 [N] or NULL
  *   y          device [M, N], element type dtype; overlaps no input
  *   stream     cudaStream_t; asynchronous, no workspace.
