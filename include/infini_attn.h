@@ -309,8 +309,8 @@ INFINI_API int infini_attn_rope_tables(float* cos_out, float* sin_out, int n_pos
  *   group      32, 64 or 128
  * K must be a multiple of 8 (INFINI_ERR_UNSUPPORTED).
  *
- * infini_attn_w4_quantize rounds w [N, K] (element type dtype, finite) to the
- * nearest codes: with zeros, scale = bf16(range / 15) of the group's values
+ * infini_attn_w4_quantize rounds w [N, K] (element type dtype, |w| <= 2^126, so
+ * that a group's range and 15 rounded scales lie within fp32) to the nearest codes: with zeros, scale = bf16(range / 15) of the group's values
  * and 0, zero = round(-low / scale); without, scale = bf16(max |w| / 7).
  * infini_attn_w4_pack lays out codes a caller has (uint8 [N, K]; bits above
  * the lowest four are dropped).  infini_attn_w4_dequantize writes w [N, K].
