@@ -1087,6 +1087,7 @@ int q4_layout(const infini_dims_t* d, int seg_len, Q4Layout* lay) {
   if (d->d_k != d->d_v || !head_dim_ok(d->d_k) || (long long)d->B * d->H_q > kQ4MostHeads || seg_len > (1 << 30))
     return INFINI_ERR_UNSUPPORTED;
   const int zc = q4_head_chunks(d->H_q / d->H_kv);
+  if (!q4_units_ok(d->B, d->H_q, d->H_kv, seg_len)) return INFINI_ERR_UNSUPPORTED;
   lay->tickets = (size_t)d->B * d->H_kv * zc * 4;  // (at most one for each query head)
   lay->total = align_up(kQ4TicketBytes + q4_partial_bytes(d->B, d->H_q, d->H_kv, seg_len, d->d_k));
   return INFINI_OK;

@@ -224,6 +224,8 @@ struct Q4Problem {
 };
 enum class Q4What { kStep, kAppend, kRead };
 int q4_head_chunks(int g);
+// Whether the kernel can count the step's units of work (they take 32 bits).
+bool q4_units_ok(int B, int H_q, int H_kv, int S);
 size_t q4_partial_bytes(int B, int H_q, int H_kv, int S, int d);
 cudaError_t launch_q4(const Q4Problem& p, Q4What what, int n, void* k, void* v, cudaStream_t stream);
 

@@ -1297,6 +1297,10 @@ cudaError_t launch_type(const Q4Problem& p, Q4What what, int n, void* k, void* v
 
 int q4_head_chunks(int g) { return chunks_of(g); }
 
+bool q4_units_ok(int B, int H_q, int H_kv, int S) {
+  return (long long)B * H_kv * chunks_of(H_q / H_kv) * (kLeadUnits + S / kUnit + 1) <= 0x7fffffffLL;
+}
+
 // Bytes of the partials: one per query head, and two sets of kHeads per CTA.
 size_t q4_partial_bytes(int B, int H_q, int H_kv, int S, int d) {
   return ((size_t)B * H_q + (size_t)q4_plan(B, H_q, H_kv, S).ctas * 2 * kHeads) * (2 * d + 4) * 4;

@@ -578,6 +578,8 @@ INFINI_API size_t infini_attn_decode_q4_workspace_bytes(const infini_dims_t* dim
  *                (see there), or NULL with workspace_bytes == 0
  *                (stream-ordered allocation, zeroed by the call)
  *   stream       cudaStream_t; asynchronous.
+ * Work of more than 2^31 units (of 128 rows of a stream's KV head, for each 8 of its query
+ * heads) is refused (INFINI_ERR_UNSUPPORTED).
  * The buffer's arrays, out_t and the workspace overlap nothing.  Sums run in a
  * fixed order: repeated calls are bitwise equal.  The order follows from all the
  * positions (streams share the GPU by their lengths), so a stream's last bits

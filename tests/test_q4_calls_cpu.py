@@ -42,3 +42,21 @@ def test_alignment_of_a_rows_part(lib, d):
     assert append(cache(8, "k_codes"), k=over) == api.ERR_ALIGN
     assert append(cache(0), pos=7 * MB + 4, k=over) == api.ERR_ALIAS
     assert append(cache(0), pos=7 * MB + 2, k=over) == api.ERR_ALIGN
+
+
+def test_more_units_of_work_than_32_bits_count_are_refused(lib):
+    """A decode step whose 128-row units, one set for every 8 query heads of a KV head,
+    pass 2^31 has no workspace and is refused."""
+    def need(B, H_q, H_kv, seg):
+        return lib.infini_attn_decode_q4_workspace_bytes(ctypes.byref(api.make_dims(B, H_q, H_kv, 1, 32, 32, 1)), seg)
+
+    assert need(1, 65528, 1, 1 << 26) == 0      # 8191 (2^19 + 9) units
+    assert need(1, 65528, 1, 1 << 24) > 0
+    assert need(1, 65528, 65528, 1 << 20) > 0   # 65528 (2^13 + 9)
+    assert need(7, 9362, 9362, 1 << 30) == 0
+    assert need(1, 8, 1, 1 << 30) > 0
+    d = ctypes.byref(api.make_dims(1, 65528, 1, 1, 32, 32, 1))
+    MB = 1 << 20
+    cache = ctypes.byref(api._CacheQ4Ptrs(1 << 40, 2 << 40, 3 << 40, 4 << 40))
+    assert lib.infini_attn_decode_step_q4(5 * MB, 15 * MB, 16 * MB, 17 * MB, cache, 18 * MB, 19 * MB, 20 * MB, 1 << 26, d,
+                                          30 * MB, None, 0, None) == api.ERR_UNSUPPORTED
