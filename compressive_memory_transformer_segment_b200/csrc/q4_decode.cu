@@ -443,8 +443,8 @@ __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) <
 // counts by the codes, which all lie on one side of zero (bf16 heads, 2048 rows: 4e-4 of
 // the output against 2e-5).  With at most 4 query heads per KV head and one part per
 // query (kPaired) the second parts take the columns of heads 4 .. 7, whose lanes hold the
-// same four heads again: 64 streams 111 us, against 107 with one part and 125 with
-// two products.
+// same four heads again: 64 streams of 4 heads 112 us, against 107 with one part and 125 with
+// two products.  (8 heads: 124 us by two products, 110 with one part.)
 // The weights' range is a power of two for each head and group (`unit`): their largest
 // so far lies at 2^8 .. 2^15 (lower() and rebase() see to it), so that what fp16
 // drops, 2^-24, is 2^-32 of it or less, whatever the scales of other groups, of rows of
@@ -468,8 +468,8 @@ struct Attention {
   float f1, f2[2];         // log2(e) / sqrt(d) kUnit1, 2^-e: scores to powers of two
   float m[2], l[2];        // reference of the powers; their sum over this lane's rows
   float o[2 * NJ][4];      // O^T without the minima, times unit / kUnit1 (rows i + 8: over kOdd too)
-  float2 omin[NJ];         // sum of p (minimum + kCenter scale) over this lane's rows
-  float2 unit[NJ];         // powers of two: p scale unit is what group j's products get
+  float omin[NJ][2];       // sum of p (minimum + kCenter scale) over this lane's rows
+  float unit[NJ][2];       // powers of two: p scale unit is what group j's products get
   float minus;             // kPaired: 0 in the lanes of the first parts, -1 of the second
 
   // q_t: this KV head's first query; ng: heads of it that exist.
@@ -544,8 +544,8 @@ struct Attention {
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      omin[j] = both<float2>(0.f);
-      unit[j] = both<float2>(kMostUnit);
+      omin[j][0] = omin[j][1] = 0.f;
+      unit[j][0] = unit[j][1] = kMostUnit;
 #pragma unroll
       for (int k = 0; k < 4; ++k) o[2 * j][k] = o[2 * j + 1][k] = 0.f;
     }
@@ -573,12 +573,10 @@ struct Attention {
       l[h] *= corr;
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
-        float& u = h ? unit[j].y : unit[j].x;
-        float& om = h ? omin[j].y : omin[j].x;
-        const float to = fminf(u * grow, kMostUnit);
-        om *= corr;
-        scale_o(j, h, corr * (to * inverse(u)));
-        u = to;
+        const float to = fminf(unit[j][h] * grow, kMostUnit);
+        omin[j][h] *= corr;
+        scale_o(j, h, corr * (to * inverse(unit[j][h])));
+        unit[j][h] = to;
       }
     }
   }
@@ -597,11 +595,10 @@ struct Attention {
           top = fmaxf(top, w < INFINITY ? w : 0.f);  // (a lost group or score has no say)
         }
         top = column_max(top);
-        float& u = h ? unit[j].y : unit[j].x;
-        if (top * 0x1p-7f * u >= 1.f) {
+        if (top * 0x1p-7f * unit[j][h] >= 1.f) {
           const float to = pow2(127 - (__float_as_int(top) >> 23));
-          scale_o(j, h, to * inverse(u));
-          u = to;
+          scale_o(j, h, to * inverse(unit[j][h]));
+          unit[j][h] = to;
         }
       }
   }
@@ -644,16 +641,18 @@ struct Attention {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const float sc = t.vp[e].scale(j);
-        float2 x = mul(mul({pr[2 * e], pr[2 * e + 1]}, unit[j]), {sc, sc});
+        float x[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) x[h] = pr[2 * e + h] * unit[j][h] * sc;
         if constexpr (kPaired) {
           // The leading 11 bits (which is what truncating to fp16 leaves), or the rest.
-          const float2 lead = {__uint_as_float(__float_as_uint(x.x) & 0xffffe000u),
-                               __uint_as_float(__float_as_uint(x.y) & 0xffffe000u)};
-          x = fma(lead, {minus, minus}, x);
-          asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(w[j][e][0]) : "f"(x.y), "f"(x.x));
+          const float2 lead = {__uint_as_float(__float_as_uint(x[0]) & 0xffffe000u),
+                               __uint_as_float(__float_as_uint(x[1]) & 0xffffe000u)};
+          const float2 part = fma(lead, {minus, minus}, {x[0], x[1]});
+          asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(w[j][e][0]) : "f"(part.y), "f"(part.x));
         } else {
 #pragma unroll
-          for (int part = 0; part < VP; ++part) w[j][e][part] = split_f16(x.x, x.y);
+          for (int part = 0; part < VP; ++part) w[j][e][part] = split_f16(x[0], x[1]);
         }
       }
   }
@@ -680,7 +679,8 @@ struct Attention {
       for (int e = 0; e < 2; ++e) {
         const float sc = t.vp[e].scale(j);
         const float mn = kExact ? fmaf(kCenter, sc, t.vp[e].minimum(j)) : t.vp[e].minimum(j);
-        omin[j] = fma({pr[2 * e], pr[2 * e + 1]}, {mn, mn}, omin[j]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) omin[j][h] = fmaf(pr[2 * e + h], mn, omin[j][h]);
       }
 #pragma unroll
       for (int part = 0; part < VP; ++part) {
@@ -1076,8 +1076,7 @@ q4_decode_kernel(Q4Problem p) {
         }
 #pragma unroll
         for (int j = 0; j < D / 32; ++j) {
-          const float add = column_sum(h ? at.omin[j].y : at.omin[j].x);
-          const float unit = at.inverse(h ? at.unit[j].y : at.unit[j].x);
+          const float add = column_sum(at.omin[j][h]), unit = at.inverse(at.unit[j][h]);
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             float* to = &red[warp][2 * c + h][32 * j + 4 * i + 2 * k];
