@@ -30,14 +30,15 @@ __device__ __forceinline__ void unpack_codes(uint32_t w, uint32_t bias, uint32_t
   }
 }
 
-// The leading 8 bits of (lo, hi) as bf16x2, and what they leave: three such steps
-// hold all 24 bits of an fp32 (down to 2^-133, bf16's least value).  Truncated, not
-// rounded: fp32's largest values would round to infinity.
+// bf16x2 of (lo, hi), and what it leaves of them: lo and hi become the
+// rounding errors.  Three such steps hold all 24 bits of an fp32 (down to 2^-133, bf16's
+// least value).  Saturated: fp32's largest values would round to infinity.
 __device__ __forceinline__ uint32_t split_bf16(float& lo, float& hi) {
-  const uint32_t a = __float_as_uint(lo), b = __float_as_uint(hi);
-  lo -= __uint_as_float(a & 0xffff0000u);
-  hi -= __uint_as_float(b & 0xffff0000u);
-  return __byte_perm(a, b, 0x7632);
+  uint32_t v;
+  asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(v) : "f"(hi), "f"(lo));
+  lo -= __uint_as_float(v << 16);
+  hi -= __uint_as_float(v & 0xffff0000u);
+  return v;
 }
 
 // c += a b: a 16 x 16 (rows x k), b 16 x 8 (k x columns), bf16 with fp32

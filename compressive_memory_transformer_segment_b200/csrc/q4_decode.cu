@@ -26,8 +26,8 @@
 // (no barrier), three tiles ahead.
 //
 // Measured (device time): 2 streams at the end of 2048-row segments, 32/8 heads of
-// 128, 14 us (6 MB: latency alone); 64 streams at ragged positions below 8192 111
-// us for 370 MB, 3.3 TB/s, 0.51 of the copy rate; 8 x 8 x 1500 rows appended and read
+// 128, 14 us (6 MB: latency alone); 64 streams at ragged positions below 8192 112
+// us for 370 MB, 3.3 TB/s, 0.50 of the copy rate; 8 x 8 x 1500 rows appended and read
 // back 34 us for 137 MB, 4.0 TB/s (bound by the instructions that choose the codes).
 //
 // Grid: the rows of all (stream, KV head, chunk of 8 query heads) are shared out
@@ -54,8 +54,16 @@ constexpr int kHeads = 8;               // query heads of a CTA (columns of a pr
 constexpr int kUnit = kWarps * 32;      // rows of the smallest share of the work
 constexpr int kSMs = 148;
 // What a segment costs besides its rows, in units of 128 rows (the latencies of
-// its first loads and its partial's way to the workspace): 64 streams at ragged
-// positions below 8192 take 145 us with 2, 121 with 4, 105 with 8, 112 with 12.
+// its first loads, the memory's rows and its partial's way to the workspace), for every
+// shape: 64 streams at ragged positions below 8192, us with 2 / 4 / 8 / 12 / 20:
+//   4 heads per KV head, d = 128   148 / 123 / 113 / 119 / 122
+//   d = 64                         103 /  78 /  69 /  73 /  77
+//   d = 32                          69 /  59 /  50 /  52 /  58
+//   1 head per KV head             139 / 116 / 111 / 117 / 120
+//   8 heads per KV head            179 / 145 / 128 / 135 / 139
+//   fp32 heads, d = 128            200 / 196 / 197 / 201 / 207
+//   fp32 heads, d = 64             144 / 128 / 125 / 128 / 131
+// and 256 streams below 1024, d = 128: 153 / 132 / 123 / 124 / 130.
 constexpr int kLeadUnits = 8;
 constexpr int kResident = 3;  // CTAs per SM (bf16 heads; two for fp32 ones)
 

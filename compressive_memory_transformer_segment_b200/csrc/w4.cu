@@ -129,12 +129,17 @@ __device__ __forceinline__ int tile_row(const W4Problem& p, int tile, int m) {
 }
 
 // A row tile's codes of a block (rows a and b of this lane) times NT token tiles,
-// into acc; piece(j, f): the tokens' fragments of channels 32 j ...
+// into acc; piece(j, f): the tokens' fragments of channels 32 j ...  The second and
+// third parts of fp32 tokens have a sum of their own, added to the first's once a group:
+// the tensor cores truncate every sum, the small ones then at 2^-8 of the large (128
+// channels: error 2.4e-7 with one sum, 4e-8 with two; 64 tokens, 4096 -> 16384: 157 and 134
+// us, the two being chains that do not wait for each other).
 template <typename T, int NT, int NG, typename F>
 __device__ __forceinline__ void multiply(const uint4& a, const uint4& b, const GroupParams<NG>& pa,
                                          const GroupParams<NG>& pb, F&& piece, float (&acc)[NT][4]) {
   const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
-  float s[NT][4];
+  constexpr bool kParts = TokenFrag<T>::kParts > 1;
+  float s[NT][4], small[kParts ? NT : 1][4];
   uint32_t ba = 0, bb = 0;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -158,8 +163,17 @@ __device__ __forceinline__ void multiply(const uint4& a, const uint4& b, const G
       mma_bf16(s[n], fa[2], fb[2], fa[3], fb[3], f[n].b[0][2], f[n].b[0][3]);
 #pragma unroll
       for (int part = 1; part < TokenFrag<T>::kParts; ++part) {
-        mma_bf16(s[n], fa[0], fb[0], fa[1], fb[1], f[n].b[part][0], f[n].b[part][1]);
-        mma_bf16(s[n], fa[2], fb[2], fa[3], fb[3], f[n].b[part][2], f[n].b[part][3]);
+        if (first && part == 1)
+          mma_bf16_first(small[n], fa[0], fb[0], fa[1], fb[1], f[n].b[part][0], f[n].b[part][1]);
+        else
+          mma_bf16(small[n], fa[0], fb[0], fa[1], fb[1], f[n].b[part][0], f[n].b[part][1]);
+        mma_bf16(small[n], fa[2], fb[2], fa[3], fb[3], f[n].b[part][2], f[n].b[part][3]);
+      }
+      if constexpr (kParts) {
+        if (last) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[n][e] += small[n][e];
+        }
       }
       if (last) {
         const float sa = pa.scale(g), sb = pb.scale(g);
@@ -342,7 +356,7 @@ w4_split_kernel(W4Problem p) {
 // A CTA per 64 rows, one tile a warp, all blocks in turn: the tokens' channels of
 // a block are copied to shared memory once for the four tiles, two blocks ahead
 // (one ahead for 64 fp32 tokens, whose blocks are 32 KB: with three slots two CTAs
-// fit an SM, with four one, and 4096 -> 16384 takes 162 us against 311), and a
+// fit an SM, with four one, and 4096 -> 16384 takes 134 us, 162 against 311 when that was measured), and a
 // warp's codes are loaded three blocks ahead into registers.
 constexpr int kRowWarps = 4;
 template <typename T, int NT>
@@ -448,9 +462,16 @@ w4_rows_kernel(W4Problem p) {
 template <typename T, int NT, int NG>
 cudaError_t launch_tokens(const W4Problem& p, cudaStream_t st) {
   const unsigned tiles = (p.N + kTile - 1) / kTile, passes = (p.M + NT * 8 - 1) / (NT * 8);
-  // 64 rows a CTA where that gives every SM one: 16 tokens, 4096 -> 16384 take
-  // 21 us so and 25 us with the blocks shared out, 64 tokens 42 and 79.  With 8 tokens or
-  // fewer there is little to share, and the split is as fast or faster.
+  // 64 rows a CTA where that gives every SM one.  bf16 tokens, 4096 channels, us with 64
+  // rows a CTA / with the blocks shared out:
+  //   tokens         16            17            32            64
+  //   4096 rows   15.0 /  6.3   19.1 /  9.5   19.3 / 11.4   30.1 / 23.1
+  //   6144 rows   16.5 / 10.5   20.4 / 13.2   20.7 / 16.2   31.1 / 33.5
+  //   16384 rows  20.8 / 21.8   26.6 / 32.9   27.2 / 38.6   42.0 / 79.1
+  // and fp32 tokens:
+  //   6144 rows   32.3 / 17.0   64.5 / 29.8   66.1 / 30.9  116.5 / 87.5
+  //   16384 rows  43.5 / 38.2   72.3 / 72.8   73.9 / 75.6  134.1 / 216.1
+  // With 8 tokens or fewer there is little to share, and the split is as fast or faster.
   if constexpr (NT > 1) {
     if (tiles >= (unsigned)(kRowWarps * kSMs)) {
       constexpr int copies = kRowStages<T, NT> * NT * 8 * kBlock * (int)sizeof(T), sums = kRowWarps * kTile * (NT * 8 + 1) * 4;

@@ -386,7 +386,9 @@ INFINI_API int infini_attn_qkv_project_w4(const void* x, const void* packed, con
  * Rows do not affect one another.  Squares are summed in fp32: |values|
  * beyond 1e18 overflow the mean.  Supported: width <= 16384
  * (INFINI_ERR_UNSUPPORTED beyond); rows whose byte size is a multiple of 16
- * are read in 16-byte pieces, others element by element.  Errors:
+ * are read in 16-byte pieces, of 4 in 4-byte pieces, others element by element.
+ * sg(gate) is held to 2^-20 (fp32 rows) and 2^-17 (bf16 rows, whose own digits
+ * end at 2^-8).  Errors:
  * INFINI_ERR_ARG (NULL r, a size < 1, eps, gate / scale / w_post / rstd
  * without what they belong to, a missing or extra output),
  * INFINI_ERR_ALIGN, INFINI_ERR_ALIAS (any overlap of an output but r_out ==
@@ -448,7 +450,8 @@ INFINI_API int infini_attn_block_norm_backward(const void* dr_out, const void* d
  * Bytes of device workspace infini_attn_decode_step needs (0 if the sizes are
  * invalid; dims->L is ignored).  The workspace starts with the step's ticket
  * counters: a workspace must be zero-filled before its first decode step
- * (each step leaves the counters at zero again); the rest is scratch. */
+ * (each step leaves the counters at zero again), and again before a step of other
+ * sizes; the rest is scratch. */
 INFINI_API size_t infini_attn_decode_workspace_bytes(const infini_dims_t* dims, int seg_len,
                                                      int rule);
 
@@ -580,6 +583,13 @@ INFINI_API size_t infini_attn_decode_q4_workspace_bytes(const infini_dims_t* dim
  *   stream       cudaStream_t; asynchronous.
  * Work of more than 2^31 units (of 128 rows of a stream's KV head, for each 8 of its query
  * heads) is refused (INFINI_ERR_UNSUPPORTED).
+ * Arithmetic: sums and the softmax's statistics in fp32; the products with the codes
+ * take fp16 parts.  fp32 heads: two parts for the queries and for probability times
+ * scale (2^-22 of each).  bf16 heads: the queries exactly (elements below 2^-29 of a
+ * head's largest in fewer bits), probability times scale to 2^-21, and of a product of 16
+ * terms what lies 2^-13 of a code below the largest is dropped (about 2^-16 of the sum).
+ * What is kept of one group of value channels, for one head, does not depend on the
+ * size of other groups, nor on what other heads attend to.
  * The buffer's arrays, out_t and the workspace overlap nothing.  Sums run in a
  * fixed order: repeated calls are bitwise equal.  The order follows from all the
  * positions (streams share the GPU by their lengths), so a stream's last bits

@@ -19,8 +19,8 @@ def test_fp32_tokens_of_every_size(cuda_lib, M, N):
     (beyond bf16's largest, which would round to infinity), times an integer -1, 0 or 1 and a
     scale 2^-10 or 2^10: exact but for three additions and one product of 2^-23, and for what
     lies below the types' least values.  Those are 2^-149 for the result, and 2^-133 for a
-    token's bf16 parts (8 exponent bits like fp32's, 7 bits of mantissa: 2^-126 2^-7): truncating a
-    part leaves less than that of the token, which counts times |q - z| = 1 and the scale."""
+    token's bf16 parts (8 exponent bits like fp32's, 7 bits of mantissa: 2^-126 2^-7): rounding the
+    parts leaves less than that of the token, which counts times |q - z| = 1 and the scale."""
     K, group = 136, 32
     r = np.random.default_rng(1)
     code = r.integers(7, 10, (N, K)).astype(np.uint8)
