@@ -453,6 +453,9 @@ __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) <
 // query (kPaired) the second parts take the columns of heads 4 .. 7, whose lanes hold the
 // same four heads again: 64 streams of 4 heads 112 us, against 107 with one part and 125 with
 // two products.  (8 heads: 124 us by two products, 110 with one part.)
+// fp32 heads add a tile's products, and the second parts' of a score, to their sums by
+// fp32 additions: the tensor cores truncate the sums they go on with (2048 rows: error 5.1e-7
+// against 2.5e-7; 64 streams 197 against 202 us).
 // The weights' range is a power of two for each head and group (`unit`): their largest
 // so far lies at 2^8 .. 2^15 (lower() and rebase() see to it), so that what fp16
 // drops, 2^-24, is 2^-32 of it or less, whatever the scales of other groups, of rows of
@@ -628,8 +631,11 @@ struct Attention {
       mma_f16(d, fa[2], fb[2], fa[3], fb[3], qf[j][0][2], qf[j][0][3]);
 #pragma unroll
       for (int part = 1; part < NP; ++part) {
-        mma_f16(d, fa[0], fb[0], fa[1], fb[1], qf[j][part][0], qf[j][part][1]);
-        mma_f16(d, fa[2], fb[2], fa[3], fb[3], qf[j][part][2], qf[j][part][3]);
+        float small[4];
+        mma_f16_first(small, fa[0], fb[0], fa[1], fb[1], qf[j][part][0], qf[j][part][1]);
+        mma_f16(small, fa[2], fb[2], fa[3], fb[3], qf[j][part][2], qf[j][part][3]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) d[e] += small[e];
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -693,8 +699,16 @@ struct Attention {
 #pragma unroll
       for (int part = 0; part < VP; ++part) {
         const uint32_t b0 = transpose8(w[j][0][part]), b1 = transpose8(w[j][1][part]);
-        mma_f16(o[2 * j], lo[0], lo[1], hi[0], hi[1], b0, b1);
-        mma_f16(o[2 * j + 1], lo[2], lo[3], hi[2], hi[3], b0, b1);
+        if constexpr (kExact) {
+          float t[2][4];
+          mma_f16_first(t[0], lo[0], lo[1], hi[0], hi[1], b0, b1);
+          mma_f16_first(t[1], lo[2], lo[3], hi[2], hi[3], b0, b1);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[2 * j + e / 4][e % 4] += t[e / 4][e % 4];
+        } else {
+          mma_f16(o[2 * j], lo[0], lo[1], hi[0], hi[1], b0, b1);
+          mma_f16(o[2 * j + 1], lo[2], lo[3], hi[2], hi[3], b0, b1);
+        }
       }
     }
   }
