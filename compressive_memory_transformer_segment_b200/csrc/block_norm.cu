@@ -25,9 +25,9 @@
 // packed operations on two neighbouring channels (backward, 16384 x 4096: 209 us,
 // 234 with single ones, whose instructions filled 60% of the cycles).
 //
-// Measured (device time, bf16, every part): forward 65536 x 4096 462 us, 5.8 TB/s;
-// backward 16384 x 4096 209 us, 5.1 TB/s, 8192 x 768 28 us, 3.6 TB/s; one token 3.3
-// us.  What keeps the backward below the copy rate: its sums and weights take the
+// Measured (device time, bf16, every part): forward 65536 x 4096 450 us, 6.0 TB/s;
+// backward 16384 x 4096 205 us, 5.2 TB/s, 8192 x 768 28 us, 3.7 TB/s; one token 3.3
+// us; fp32, 16384 x 4096: 241 and 430 us.  What keeps the backward below the copy rate: its sums and weights take the
 // registers of all but 16 warps per SM, which two reductions a row stop in turn.
 #include "common.cuh"
 #include "f32x2.cuh"
