@@ -444,8 +444,8 @@ __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) <
 // Running attention of one warp over its rows, for 8 heads: fragments of
 // heads 2c, 2c + 1.  The operands that meet the codes are fp16.
 // Queries are kept in its range by a power of two per head, set by the largest
-// element: bf16 heads in one part (exact down to 2^-29 of that), fp32 heads in two
-// (2^-22 of an element, and 2^-40 of the largest).
+// element: bf16 heads in one part (exact down to 2^-27 of that), fp32 heads in two
+// (2^-22 of an element, and 2^-39 of the largest).
 // The weights, probabilities times scale, go in as two parts (2^-22 of a weight, for
 // bf16 heads 2^-21): one part, 2^-11 at most, would be the sum's largest error, since it
 // counts by the codes, which all lie on one side of zero (bf16 heads, 2048 rows: 4e-4 of

@@ -585,7 +585,7 @@ INFINI_API size_t infini_attn_decode_q4_workspace_bytes(const infini_dims_t* dim
  * heads) is refused (INFINI_ERR_UNSUPPORTED).
  * Arithmetic: sums and the softmax's statistics in fp32; the products with the codes
  * take fp16 parts.  fp32 heads: two parts for the queries and for probability times
- * scale (2^-22 of each).  bf16 heads: the queries exactly (elements below 2^-29 of a
+ * scale (2^-22 of each).  bf16 heads: the queries exactly (elements below 2^-27 of a
  * head's largest in fewer bits), probability times scale to 2^-21, and of a product of 16
  * terms what lies 2^-13 of a code below the largest is dropped (about 2^-16 of the sum).
  * What is kept of one group of value channels, for one head, does not depend on the
